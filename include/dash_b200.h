@@ -288,7 +288,7 @@ SHAMPOO_API int shampoo_profile_reset(void);
  * for s = 0 launches of the tensor-core GEMM with 128 x 128 tiles (executed
  * tensor-core flops: 3 * 2*128*128*B per computed tile, or 1 * ... for
  * single-pass fp16 launches), 1 gather + factor EMA, 2 power iteration,
- * 3 root solver, 4 preconditioner products, 5 Adam graft + update, 6 launches
+ * 3 root solver, 4 preconditioner products, 5 Adam graft + update and AdamW steps, 6 launches
  * of the tensor-core GEMM with 128 x 256 tiles (3 * 2*128*256*B per tile), 7
  * launches of the Newton-DB kernel on resident factors of 128 (9 * 2*128^3
  * per iteration and factor);
@@ -308,6 +308,163 @@ SHAMPOO_API int shampoo_debug_inject_timeout(void);
 
 /* Free a ctx (host memory only).  NULL is ignored. */
 SHAMPOO_API void shampoo_destroy(shampoo_ctx* ctx);
+
+/* ------------------------------------------------------------------------
+ * Operators over a list of tensors: gradient norm and clipping, AdamW.
+ *
+ * The Shampoo step above takes 2-D fp32 matrices.  The calls below serve the
+ * rest of a model (norm weights, biases, embeddings, low-precision
+ * parameters) and what such a training step needs around both optimizers.
+ * Each works on a list of tensors in one launch; a tensor is `n` consecutive
+ * elements (n >= 0), of any alignment that its element type has.  Tensors
+ * whose pointers are all aligned to eight elements take 8- to 32-byte
+ * accesses, others scalar ones.
+ *
+ * A list is described once (..._init, host only), and its table is uploaded
+ * to the caller's workspace once (..._bind, 256-byte aligned); the tensors'
+ * addresses then stay fixed, and their contents may change between calls.
+ * All other calls take the same workspace (SHAMPOO_EINVAL for another one),
+ * are stream-ordered and can be captured into a CUDA graph; bind cannot
+ * (SHAMPOO_EINVAL on a capturing stream).  Calls on one workspace must not
+ * overlap.  The workspace's first word is the status word of its last norm,
+ * clip, step or load call (shampoo_read_status).
+ * ---------------------------------------------------------------------- */
+
+#define SHAMPOO_DTYPE_F32 0
+#define SHAMPOO_DTYPE_BF16 1
+#define SHAMPOO_DTYPE_F16 2
+
+#define SHAMPOO_QBLOCK 256                  /* elements that share a scale in 8-bit moments */
+#define SHAMPOO_MAX_TENSOR (1ll << 40)      /* elements of one tensor, at most */
+
+typedef struct shampoo_grads shampoo_grads;
+
+/* One gradient (device): n elements of `dtype`. */
+typedef struct {
+  int64_t n;
+  void* grad;
+  int dtype; /* SHAMPOO_DTYPE_* */
+} shampoo_grad;
+
+/* Describe a list of gradients (host only).  `workspace_bytes` (host out).
+ * Errors: SHAMPOO_EINVAL (null pointer, n_grads < 1, bad count, type or
+ * alignment, tensors that share memory). */
+SHAMPOO_API int shampoo_grads_init(shampoo_grads** out, const shampoo_grad* grads, int n_grads,
+                                   size_t* workspace_bytes);
+
+/* Upload the list's table to `ws`, which every later call takes. */
+SHAMPOO_API int shampoo_grads_bind(shampoo_grads* ctx, void* ws, size_t ws_bytes, void* stream);
+
+/* Global norm of the list: out[0] = norm = inv_scale sqrt(sum g^2) over all
+ * elements, out[1] = coef = inv_scale min(1, max_norm / norm), the factor
+ * that unscales and clips a gradient (device, 2 floats).  Sums are formed in
+ * fp64 in a fixed order, so equal gradients give equal bits.  An element that
+ * is not finite makes norm not finite and coef NaN and sets
+ * SHAMPOO_STATUS_NONFINITE.  max_norm > 0 (infinity: no clipping), inv_scale
+ * > 0 and finite (1 / loss scale). */
+SHAMPOO_API int shampoo_grad_norm(shampoo_grads* ctx, float max_norm, float inv_scale, float* out, void* ws,
+                                  size_t ws_bytes, void* stream);
+
+/* shampoo_grad_norm, then g <- coef g in place, each element rounded once to
+ * its type (for optimizers that read the gradients themselves, such as the
+ * Shampoo step).  Where coef is NaN every gradient is set to zero: a Shampoo
+ * step then leaves the parameters where they are. */
+SHAMPOO_API int shampoo_grad_clip(shampoo_grads* ctx, float max_norm, float inv_scale, float* out, void* ws,
+                                  size_t ws_bytes, void* stream);
+
+/* Free a list (host memory only).  NULL is ignored. */
+SHAMPOO_API void shampoo_grads_destroy(shampoo_grads* ctx);
+
+typedef struct shampoo_adamw shampoo_adamw;
+
+/* One parameter of an AdamW list (device pointers; grad is read, all else
+ * updated in place).  Its moments are kept
+ *  - in 32 bits (state_bits 32): m, v are n floats each; or
+ *  - in 8 bits (state_bits 8): m, v are n bytes of codes, m_scale and v_scale
+ *    one byte for each SHAMPOO_QBLOCK elements (the last block may be short).
+ *    m is held as sign and e4m3, r = sqrt(v) as unsigned e4m4 (values
+ *    (1 + M/16) 2^(E-1), or M/16 for E = 0); scale byte i stands for
+ *    2^(i - 127), the smallest power that brings the block's maximum within
+ *    448 (m) or 31744 (r).  All bytes 0 are moments of zero.  r > 0 is never
+ *    stored as 0.  Scale 255 marks a block that held a non-finite moment; the
+ *    whole block reads back as not finite.
+ * An fp32 parameter may have a 16-bit `copy` of its new value written beside
+ * it (rounded to nearest); a bf16 parameter is rounded stochastically. */
+typedef struct {
+  int64_t n;
+  void* param;      /* fp32 or bf16 */
+  const void* grad; /* fp32, bf16 or fp16 */
+  void* copy;       /* bf16 or fp16, or NULL */
+  void* m;
+  void* v;
+  uint8_t* m_scale; /* 8-bit moments only */
+  uint8_t* v_scale;
+  int param_dtype, grad_dtype, copy_dtype; /* SHAMPOO_DTYPE_* */
+  int state_bits;                          /* 32 or 8 */
+  float lr_scale;                          /* multiplies the step's lr, >= 0 */
+  float weight_decay;                      /* >= 0 */
+} shampoo_adamw_tensor;
+
+typedef struct {
+  float beta1, beta2;
+  float adam_eps; /* at least FLT_MIN */
+  uint64_t seed;  /* of the rounding draws */
+} shampoo_adamw_hparams;
+
+/* Describe a list of parameters (host only).  `workspace_bytes` (host out);
+ * `moment_elems` (host out, may be NULL): elements of the flat moments of the
+ * load and read calls, in which each tensor takes its n rounded up to a
+ * multiple of SHAMPOO_QBLOCK, in list order.
+ * Errors: SHAMPOO_EINVAL (null pointer, n_tensors < 1, bad count, type,
+ * alignment or hyper-parameter, a written buffer that shares memory with any
+ * other). */
+SHAMPOO_API int shampoo_adamw_init(shampoo_adamw** out, const shampoo_adamw_tensor* tensors, int n_tensors,
+                                   const shampoo_adamw_hparams* hp, size_t* workspace_bytes, int64_t* moment_elems);
+
+/* Upload the list's table to `ws` and set the step counter kept there to
+ * `steps_taken` (0, or where a checkpoint left off).  Moments are the
+ * caller's to initialise (zero, or shampoo_adamw_load_moments). */
+SHAMPOO_API int shampoo_adamw_bind(shampoo_adamw* ctx, int steps_taken, void* ws, size_t ws_bytes, void* stream);
+
+/* One AdamW step t of the whole list, in one launch; per element, in fp32:
+ *   g = coef grad;  m <- beta1 m + (1 - beta1) g;  v <- beta2 v + (1 - beta2) g^2;
+ *   param -= lr lr_scale ( m_hat / (sqrt(v_hat) + adam_eps) + weight_decay param ),
+ *   m_hat = m / (1 - beta1^t),  v_hat = v / (1 - beta2^t).
+ * 8-bit moments enter as the values they stand for; the update uses the new
+ * moments before they are rounded.  Moments in 8 bits and bf16 parameters are
+ * rounded stochastically: x lies between two neighbours of its format and
+ * goes to the upper one with the probability that makes the expectation x (a
+ * step changes sqrt(v) by far less than half a code's width, so that rounding
+ * to nearest would leave it where it is).  The draws are a hash of (seed, t,
+ * index in the list, element): the same call gives the same bits.
+ * `step` >= 1 is t, and sets the counter in ws; `step` = 0 continues that
+ * counter (t = previous t + 1), so that a captured step can be replayed.
+ * `lr_device` (device, 1 float, or NULL) replaces lr; `coef` (device, 1
+ * float, or NULL: 1) is shampoo_grad_norm's out + 1.  Where coef is not
+ * finite the step is not taken: nothing is written, the counter stays, and
+ * SHAMPOO_STATUS_NONFINITE is set.  That bit is also set when a moment or
+ * parameter becomes non-finite. */
+SHAMPOO_API int shampoo_adamw_step(shampoo_adamw* ctx, int step, float lr, const float* lr_device, const float* coef,
+                                   void* ws, size_t ws_bytes, void* stream);
+
+/* Set the list's moments from flat fp32 ones (device, 32-byte aligned,
+ * moment_elems each): copied, or rounded to nearest (ties to even) into 8
+ * bits.  v >= 0.  Elements behind a tensor's end are not read. */
+SHAMPOO_API int shampoo_adamw_load_moments(shampoo_adamw* ctx, const float* m, const float* v, void* ws,
+                                           size_t ws_bytes, void* stream);
+
+/* The list's moments as flat values (device, 32-byte aligned, moment_elems
+ * each) of `dtype`, fp32 or bf16; elements behind a tensor's end are written
+ * as zeros. */
+SHAMPOO_API int shampoo_adamw_read_moments(shampoo_adamw* ctx, void* m, void* v, int dtype, void* ws, size_t ws_bytes,
+                                           void* stream);
+
+/* Synchronise `stream` and read the step counter of `ws` (host out). */
+SHAMPOO_API int shampoo_adamw_steps_taken(const shampoo_adamw* ctx, const void* ws, size_t ws_bytes, void* stream,
+                                          int* steps_taken);
+
+/* Free a list (host memory only).  NULL is ignored. */
+SHAMPOO_API void shampoo_adamw_destroy(shampoo_adamw* ctx);
 
 #ifdef __cplusplus
 }

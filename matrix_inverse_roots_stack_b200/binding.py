@@ -26,6 +26,10 @@ SOLVER_COUPLED_NEWTON = 2
 SCALING_SPECTRAL = 0
 SCALING_FROBENIUS = 1
 PI_STARTS = 32
+DTYPE_F32 = 0
+DTYPE_BF16 = 1
+DTYPE_F16 = 2
+QBLOCK = 256  # elements that share a scale in 8-bit moments
 
 
 class ShampooError(RuntimeError):
@@ -49,6 +53,23 @@ class ShampooHParams(ctypes.Structure):
                 ("cn_fp16", ctypes.c_int)]
 
 
+class ShampooGrad(ctypes.Structure):
+    _fields_ = [("n", ctypes.c_int64), ("grad", ctypes.c_void_p), ("dtype", ctypes.c_int)]
+
+
+class AdamwTensor(ctypes.Structure):
+    _fields_ = [("n", ctypes.c_int64), ("param", ctypes.c_void_p), ("grad", ctypes.c_void_p),
+                ("copy", ctypes.c_void_p), ("m", ctypes.c_void_p), ("v", ctypes.c_void_p),
+                ("m_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p), ("param_dtype", ctypes.c_int),
+                ("grad_dtype", ctypes.c_int), ("copy_dtype", ctypes.c_int), ("state_bits", ctypes.c_int),
+                ("lr_scale", ctypes.c_float), ("weight_decay", ctypes.c_float)]
+
+
+class AdamwHParams(ctypes.Structure):
+    _fields_ = [("beta1", ctypes.c_float), ("beta2", ctypes.c_float), ("adam_eps", ctypes.c_float),
+                ("seed", ctypes.c_uint64)]
+
+
 def make_hparams(block_size=1024, beta=0.95, eps=1e-6, init_scale=1e-6, beta1=0.9, beta2=0.999,
                  adam_eps=1e-8, lr=1e-3, solver=SOLVER_NEWTON_DB, ndb_iters1=14, ndb_iters2=14,
                  cheb_degree=16, cheb_delta=1e-3, pi_starts=PI_STARTS, pi_iters=10, root_every=1,
@@ -56,6 +77,10 @@ def make_hparams(block_size=1024, beta=0.95, eps=1e-6, init_scale=1e-6, beta1=0.
     return ShampooHParams(block_size, beta, eps, init_scale, beta1, beta2, adam_eps, lr, solver,
                           ndb_iters1, ndb_iters2, cheb_degree, cheb_delta, pi_starts, pi_iters, root_every,
                           scaling, cn_iters, cn_fp16)
+
+
+def make_adamw_hparams(beta1=0.9, beta2=0.999, adam_eps=1e-8, seed=0):
+    return AdamwHParams(beta1, beta2, adam_eps, seed)
 
 
 _lib = None
@@ -79,6 +104,19 @@ _PROTOS = {
     "shampoo_strerror": (ctypes.c_char_p, [_I]),
     "shampoo_destroy": (None, [_VP]),
     "shampoo_inv_root_newton_db_static": (_I, [_VP, _VP, _I, _I, _I, _I, _F, _VP, _I, _VP, _VP]),
+    "shampoo_grads_init": (_I, [ctypes.POINTER(_VP), ctypes.POINTER(ShampooGrad), _I, ctypes.POINTER(_SZ)]),
+    "shampoo_grads_bind": (_I, [_VP, _VP, _SZ, _VP]),
+    "shampoo_grad_norm": (_I, [_VP, _F, _F, _VP, _VP, _SZ, _VP]),
+    "shampoo_grad_clip": (_I, [_VP, _F, _F, _VP, _VP, _SZ, _VP]),
+    "shampoo_grads_destroy": (None, [_VP]),
+    "shampoo_adamw_init": (_I, [ctypes.POINTER(_VP), ctypes.POINTER(AdamwTensor), _I, ctypes.POINTER(AdamwHParams),
+                                ctypes.POINTER(_SZ), ctypes.POINTER(ctypes.c_int64)]),
+    "shampoo_adamw_bind": (_I, [_VP, _I, _VP, _SZ, _VP]),
+    "shampoo_adamw_step": (_I, [_VP, _I, _F, _VP, _VP, _VP, _SZ, _VP]),
+    "shampoo_adamw_load_moments": (_I, [_VP, _VP, _VP, _VP, _SZ, _VP]),
+    "shampoo_adamw_read_moments": (_I, [_VP, _VP, _VP, _I, _VP, _SZ, _VP]),
+    "shampoo_adamw_steps_taken": (_I, [_VP, _VP, _SZ, _VP, ctypes.POINTER(_I)]),
+    "shampoo_adamw_destroy": (None, [_VP]),
     "shampoo_debug_inject_timeout": (_I, []),
     "shampoo_profile_enable": (_I, [_I]),
     "shampoo_profile_reset": (_I, []),
@@ -321,3 +359,264 @@ class Shampoo:
         if ctx is not None and _lib is not None:
             _lib.shampoo_destroy(ctx)
             self._ctx = None
+
+
+# --------------------------------------------------------------------------
+# operators over a list of tensors: gradient norm and clipping, AdamW
+# --------------------------------------------------------------------------
+
+def _dtype_code(t):
+    import torch
+    return {torch.float32: DTYPE_F32, torch.bfloat16: DTYPE_BF16, torch.float16: DTYPE_F16}.get(t.dtype)
+
+
+def _check_list(tensors, what, dtypes, device, like=None):
+    """Contiguous CUDA tensors of one device and of the given types; `like`:
+    tensors whose shapes they have."""
+    for i, t in enumerate(tensors):
+        if t.dtype not in dtypes or not t.is_cuda or t.device != device or not t.is_contiguous():
+            raise ValueError(f"{what}[{i}] must be a contiguous tensor on {device} of type "
+                             f"{' or '.join(str(d) for d in dtypes)}")
+        if like is not None and t.shape != like[i].shape:
+            raise ValueError(f"{what}[{i}] has shape {tuple(t.shape)}, not {tuple(like[i].shape)}")
+
+
+class _TensorList:
+    """What the operators over a list of tensors share: the library's list,
+    its workspace, and the streams it is used on."""
+
+    _destroy = None
+
+    def _adopt(self, ctx, ws_bytes, owned):
+        import torch
+        self._ctx = ctx
+        self.ws = _workspace(ws_bytes, self.device)
+        self._ws_args = (_ptr(self.ws), self.ws.numel())
+        self._owned = [self.ws] + owned
+        self._streams = {torch.cuda.current_stream(self.device).cuda_stream}
+
+    def _call(self, where, fn, args, stream, *passed):
+        """Run a library call on the list's device, on `stream` (default: that
+        device's current stream).  passed: the caller's tensors it works on."""
+        import torch
+        if stream is None:
+            stream = torch.cuda.current_stream(self.device)
+        elif stream.device != self.device:
+            raise ValueError(f"the stream is on {stream.device}, the tensors are on {self.device}")
+        else:
+            for t in passed:
+                t.record_stream(stream)
+        raw = stream.cuda_stream
+        if raw not in self._streams:
+            # memory made here is not handed out again before this stream is done with it
+            for t in self._owned:
+                t.record_stream(stream)
+            self._streams.add(raw)
+        if torch.cuda.current_device() == self.device.index:
+            rc = fn(*args, ctypes.c_void_p(raw))
+        else:
+            with torch.cuda.device(self.device):
+                rc = fn(*args, ctypes.c_void_p(raw))
+        if rc != SHAMPOO_OK:
+            raise ShampooError(rc, where)
+
+    def _scalar(self, t, what):
+        import torch
+        if t.dtype != torch.float32 or t.numel() != 1 or t.device != self.device:
+            raise ValueError(f"{what} must be one fp32 value on {self.device}")
+        return _ptr(t)
+
+    def status(self, stream=None):
+        """Synchronise and return (code, flags) of the last call."""
+        import torch
+        return read_status(self.ws, torch.cuda.current_stream(self.device) if stream is None else stream)
+
+    def __del__(self):
+        ctx = getattr(self, "_ctx", None)
+        if ctx is not None and _lib is not None:
+            getattr(_lib, self._destroy)(ctx)
+            self._ctx = None
+
+
+class GradClip(_TensorList):
+    """Global norm and clipping of a list of CUDA gradients (fp32, bf16 or
+    fp16, any shapes).  The gradients' addresses are fixed here, their values
+    are read at every call.  Results stay on the device, in :attr:`out`:
+    [norm, coef], with coef = inv_scale min(1, max_norm / norm), NaN where the
+    norm is not finite."""
+
+    _destroy = "shampoo_grads_destroy"
+
+    def __init__(self, grads):
+        import torch
+        self.grads = list(grads)
+        if not self.grads:
+            raise ValueError("no gradients")
+        self.device = self.grads[0].device
+        _check_list(self.grads, "grads", (torch.float32, torch.bfloat16, torch.float16), self.device)
+        arr = (ShampooGrad * len(self.grads))()
+        for i, g in enumerate(self.grads):
+            arr[i] = ShampooGrad(g.numel(), g.data_ptr(), _dtype_code(g))
+        ctx, nbytes = ctypes.c_void_p(), ctypes.c_size_t(0)
+        _check(load().shampoo_grads_init(ctypes.byref(ctx), arr, len(self.grads), ctypes.byref(nbytes)),
+               "shampoo_grads_init")
+        self.out = torch.zeros(2, dtype=torch.float32, device=self.device)
+        self._adopt(ctx, nbytes.value, [self.out])
+        self._call("shampoo_grads_bind", load().shampoo_grads_bind, (ctx, *self._ws_args), None)
+        torch.cuda.current_stream(self.device).synchronize()  # ready for any stream
+
+    def norm(self, max_norm=float("inf"), inv_scale=1.0, stream=None):
+        """Fill and return :attr:`out`; the gradients are only read."""
+        self._call("shampoo_grad_norm", load().shampoo_grad_norm,
+                   (self._ctx, max_norm, inv_scale, _ptr(self.out), *self._ws_args), stream)
+        return self.out
+
+    def clip(self, max_norm, inv_scale=1.0, stream=None):
+        """:meth:`norm`, then every gradient times coef, in place (zero where
+        coef is NaN)."""
+        self._call("shampoo_grad_clip", load().shampoo_grad_clip,
+                   (self._ctx, max_norm, inv_scale, _ptr(self.out), *self._ws_args), stream)
+        return self.out
+
+
+class AdamW(_TensorList):
+    """AdamW (decoupled weight decay) over a list of CUDA parameters of any
+    shapes, one kernel launch a step.
+
+    params: fp32 or bf16 (bf16 is rounded stochastically); grads: fp32, bf16
+    or fp16.  copies: for fp32 parameters, 16-bit tensors (or None entries)
+    that receive the new values too.  state_bits: 32 or 8, for all or for each
+    parameter; moments that are not given are allocated as zeros: fp32, or
+    8-bit codes with a scale for each 256 elements.  lr_scale and weight_decay:
+    for all or for each parameter.  Addresses are fixed here; the contents may
+    change between steps.
+    """
+
+    _destroy = "shampoo_adamw_destroy"
+
+    def __init__(self, params, grads, hp=None, copies=None, state_bits=32, m=None, v=None, m_scale=None,
+                 v_scale=None, lr_scale=1.0, weight_decay=0.0, steps_taken=0):
+        import torch
+        f32, bf16, f16 = torch.float32, torch.bfloat16, torch.float16
+        self.hp = hp if hp is not None else make_adamw_hparams()
+        self.params, self.grads = list(params), list(grads)
+        n = len(self.params)
+        if not n:
+            raise ValueError("no parameters")
+        self.device = dev = self.params[0].device
+
+        def each(x, what):
+            x = list(x) if isinstance(x, (list, tuple)) else [x] * n
+            if len(x) != n:
+                raise ValueError(f"{len(x)} {what} for {n} parameters")
+            return x
+
+        self.state_bits = each(state_bits, "state_bits")
+        lr_scale, weight_decay = each(lr_scale, "lr_scale"), each(weight_decay, "weight_decay")
+        self.copies = each(copies, "copies")
+        if any(b not in (8, 32) for b in self.state_bits):
+            raise ValueError("state_bits must be 8 or 32")
+        if len(self.grads) != n:
+            raise ValueError(f"{len(self.grads)} gradients for {n} parameters")
+        _check_list(self.params, "params", (f32, bf16), dev)
+        _check_list(self.grads, "grads", (f32, bf16, f16), dev, self.params)
+        owned = []
+
+        def state(given, what, dtype, numel):
+            out = []
+            given = each(given, what)
+            for i, t in enumerate(given):
+                want = numel(i)
+                if t is None:
+                    t = torch.zeros(want, dtype=dtype(i), device=dev) if want is not None else None
+                    owned.extend([t] if t is not None else [])
+                elif want is None:
+                    raise ValueError(f"{what}[{i}] is for 8-bit moments only")
+                elif t.numel() != want:
+                    raise ValueError(f"{what}[{i}] has {t.numel()} elements, not {want}")
+                else:
+                    _check_list([t], what, (dtype(i),), dev)
+                out.append(t)
+            return out
+
+        codes = lambda i: torch.uint8 if self.state_bits[i] == 8 else f32
+        blocks = lambda i: -(-self.params[i].numel() // QBLOCK) if self.state_bits[i] == 8 else None
+        self.m = state(m, "m", codes, lambda i: self.params[i].numel())
+        self.v = state(v, "v", codes, lambda i: self.params[i].numel())
+        self.m_scale = state(m_scale, "m_scale", lambda i: torch.uint8, blocks)
+        self.v_scale = state(v_scale, "v_scale", lambda i: torch.uint8, blocks)
+        arr = (AdamwTensor * n)()
+        for i, p in enumerate(self.params):
+            c = self.copies[i]
+            if c is not None:
+                if p.dtype != f32:
+                    raise ValueError(f"copies[{i}] is for an fp32 parameter only")
+                _check_list([c], "copies", (bf16, f16), dev, [p])
+            at = lambda t: None if t is None else t.data_ptr()
+            arr[i] = AdamwTensor(p.numel(), p.data_ptr(), self.grads[i].data_ptr(), at(c), at(self.m[i]),
+                                 at(self.v[i]), at(self.m_scale[i]), at(self.v_scale[i]), _dtype_code(p),
+                                 _dtype_code(self.grads[i]), DTYPE_F32 if c is None else _dtype_code(c),
+                                 self.state_bits[i], lr_scale[i], weight_decay[i])
+        ctx, nbytes, elems = ctypes.c_void_p(), ctypes.c_size_t(0), ctypes.c_int64(0)
+        _check(load().shampoo_adamw_init(ctypes.byref(ctx), arr, n, ctypes.byref(self.hp), ctypes.byref(nbytes),
+                                         ctypes.byref(elems)), "shampoo_adamw_init")
+        self.moment_elems = elems.value
+        self._adopt(ctx, nbytes.value, owned)
+        self._call("shampoo_adamw_bind", load().shampoo_adamw_bind, (ctx, steps_taken, *self._ws_args), None)
+        torch.cuda.current_stream(dev).synchronize()  # ready for any stream
+
+    def step(self, lr=1e-3, coef=None, step=0, stream=None):
+        """One step.  lr: a number, or one fp32 value on the device (read when
+        the step runs, also from a replayed graph).  coef: one fp32 value on
+        the device that multiplies the gradients (``GradClip.out[1:]``); where
+        it is not finite the step is not taken.  step: this step's number, or
+        0 to continue the counter on the device."""
+        on_device = hasattr(lr, "data_ptr")
+        self._call("shampoo_adamw_step", load().shampoo_adamw_step,
+                   (self._ctx, step, 0.0 if on_device else lr, self._scalar(lr, "lr") if on_device else None,
+                    None if coef is None else self._scalar(coef, "coef"), *self._ws_args), stream,
+                   *([lr] if on_device else []), *([] if coef is None else [coef]))
+
+    def steps_taken(self, stream=None):
+        """Synchronise and read the step counter."""
+        t = ctypes.c_int(0)
+        fn = load().shampoo_adamw_steps_taken
+        self._call("shampoo_adamw_steps_taken", lambda *a: fn(*a, ctypes.byref(t)), (self._ctx, *self._ws_args),
+                   stream)
+        return t.value
+
+    def _flat(self, t, what, dtypes):
+        _check_list([t], what, dtypes, self.device)
+        if t.numel() != self.moment_elems:
+            raise ValueError(f"{what} has {t.numel()} elements, not {self.moment_elems}")
+        return _ptr(t)
+
+    def views(self, flat):
+        """Each parameter's part of a flat tensor of moments, in its shape."""
+        out, at = [], 0
+        for p in self.params:
+            out.append(flat[at:at + p.numel()].view(p.shape))
+            at += -(-p.numel() // QBLOCK) * QBLOCK
+        return out
+
+    def read_moments(self, dtype=None, m=None, v=None, stream=None):
+        """Both moments as flat tensors (see :meth:`views`) of fp32 (default)
+        or bf16, into m and v where given."""
+        import torch
+        if m is None:
+            m = torch.empty(self.moment_elems, dtype=dtype or torch.float32, device=self.device)
+        if v is None:
+            v = torch.empty(self.moment_elems, dtype=m.dtype, device=self.device)
+        if v.dtype != m.dtype or (dtype is not None and m.dtype != dtype):
+            raise ValueError("m and v must be of the one type asked for")
+        pm, pv = (self._flat(t, w, (torch.float32, torch.bfloat16)) for t, w in ((m, "m"), (v, "v")))
+        self._call("shampoo_adamw_read_moments", load().shampoo_adamw_read_moments,
+                   (self._ctx, pm, pv, _dtype_code(m), *self._ws_args), stream, m, v)
+        return m, v
+
+    def load_moments(self, m, v, stream=None):
+        """Set both moments from flat fp32 tensors (see :meth:`views`)."""
+        import torch
+        pm, pv = (self._flat(t, w, (torch.float32,)) for t, w in ((m, "m"), (v, "v")))
+        self._call("shampoo_adamw_load_moments", load().shampoo_adamw_load_moments,
+                   (self._ctx, pm, pv, *self._ws_args), stream, m, v)

@@ -1,0 +1,246 @@
+// Global norm and clipping of a list of gradients (shampoo_grad_norm,
+// shampoo_grad_clip in include/dash_b200.h).
+//
+// norm = inv_scale sqrt(sum g^2) over every element of every tensor, and
+// coef = inv_scale min(1, max_norm / norm), the factor that unscales and
+// clips a gradient; clipping writes g <- coef g in place.  Both are bound by
+// HBM: one read of the gradients for the norm, one more read and a write for
+// clipping.
+#include <cmath>
+#include <new>
+
+#include "profile.cuh"
+#include "tensor_list.cuh"
+
+namespace dash {
+namespace {
+
+struct GradChunk {
+  void* grad;
+  int count;   // elements, at most the list's chunk size
+  int flags;   // element type, and kVec when the start is aligned to eight elements
+};
+constexpr int kVec = 16;
+constexpr int kTypeMask = 15;
+
+// Start of the workspace.
+struct NormHeader {
+  unsigned status;  // first word: the status word
+  unsigned ticket;
+};
+constexpr size_t kHeaderBytes = 256;
+constexpr int kSteps = 4;  // warp steps in flight: a chunk is kSteps x kListWarps x 256 elements
+constexpr int kChunk = kSteps * kListWarps * kQBlock;
+
+__device__ __forceinline__ void add_squares(const float* x, double* acc) {
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const double d = x[j];
+    acc[j & 1] = fma(d, d, acc[j & 1]);
+  }
+}
+
+// Sum of a block's values, in a fixed order; valid in thread 0.
+__device__ __forceinline__ double block_sum(double x) {
+  __shared__ double part[kListWarps];
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+  if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = x;
+  __syncthreads();
+  double s = 0.0;
+  if (threadIdx.x == 0)
+    for (int w = 0; w < kListWarps; ++w) s += part[w];
+  __syncthreads();
+  return s;
+}
+
+// The squares are formed and added in fp64: the square of any finite fp32
+// value is exact and in range there, so neither small nor large gradients
+// are lost, and the result is not finite exactly when an element is not.
+// Each block adds a fixed set of chunks and the last one to finish adds the
+// blocks' sums, so that the order, and with it the result, is the same on
+// every call.  Chunks are taken from the end: what the L2 cache still holds
+// afterwards is the front of the list, where the next pass starts.
+__global__ void __launch_bounds__(kListThreads) grad_norm_kernel(const GradChunk* __restrict__ chunks, int n_chunks,
+                                                                 NormHeader* hdr, double* partial, double max_norm,
+                                                                 double inv_scale, float* out) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  double acc[2] = {0.0, 0.0};
+  for (int k = n_chunks - 1 - static_cast<int>(blockIdx.x); k >= 0; k -= gridDim.x) {
+    const GradChunk c = chunks[k];
+    const int type = c.flags & kTypeMask;
+    if ((c.flags & kVec) && c.count == kChunk) {
+      Raw8 r[kSteps];
+#pragma unroll
+      for (int s = 0; s < kSteps; ++s) load8(c.grad, (s * kListWarps + warp) * 32 + lane, type, r[s]);
+#pragma unroll
+      for (int s = 0; s < kSteps; ++s) {
+        float x[8];
+        widen8(r[s], type, x);
+        add_squares(x, acc);
+      }
+    } else {
+      for (int i = threadIdx.x; i < c.count; i += kListThreads) {
+        const double d = load1(c.grad, i, type);
+        acc[0] = fma(d, d, acc[0]);
+      }
+    }
+  }
+  const double sum = block_sum(acc[0] + acc[1]);
+  if (threadIdx.x == 0) partial[blockIdx.x] = sum;
+  if (!last_block(&hdr->ticket)) return;
+  double t = 0.0;
+  for (int i = threadIdx.x; i < static_cast<int>(gridDim.x); i += kListThreads) t += __ldcg(partial + i);
+  t = block_sum(t);
+  if (threadIdx.x == 0) {
+    const double norm = sqrt(t) * inv_scale;
+    const bool ok = isfinite(t);
+    out[0] = static_cast<float>(norm);
+    out[1] = ok ? static_cast<float>((norm > max_norm ? max_norm / norm : 1.0) * inv_scale) : __int_as_float(0x7fffffff);
+    hdr->status = ok ? 0u : kStatusNonFinite;
+  }
+}
+
+// g <- coef g; a coefficient of 1 leaves the gradients unread, one that is
+// not finite sets them to zero.
+__global__ void __launch_bounds__(kListThreads) grad_clip_kernel(const GradChunk* __restrict__ chunks, int n_chunks,
+                                                                 const float* __restrict__ out) {
+  const float coef = out[1];
+  if (coef == 1.0f) return;
+  const bool zero = not_finite(coef);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  for (int k = blockIdx.x; k < n_chunks; k += gridDim.x) {
+    const GradChunk c = chunks[k];
+    const int type = c.flags & kTypeMask;
+    if ((c.flags & kVec) && c.count == kChunk) {
+      Raw8 r[kSteps];
+#pragma unroll
+      for (int s = 0; s < kSteps; ++s) load8(c.grad, (s * kListWarps + warp) * 32 + lane, type, r[s]);
+#pragma unroll
+      for (int s = 0; s < kSteps; ++s) {
+        float x[8];
+        widen8(r[s], type, x);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) x[j] = zero ? 0.0f : x[j] * coef;
+        store8(c.grad, (s * kListWarps + warp) * 32 + lane, type, x);
+      }
+    } else {
+      for (int i = threadIdx.x; i < c.count; i += kListThreads)
+        store1(c.grad, i, type, zero ? 0.0f : load1(c.grad, i, type) * coef);
+    }
+  }
+}
+
+}  // namespace
+}  // namespace dash
+
+struct shampoo_grads {
+  std::vector<dash::GradChunk> chunks;
+  size_t off_partial = 0, total = 0;
+  const void* bound_ws = nullptr;
+  int norm_blocks = 0, clip_blocks = 0;
+};
+
+namespace {
+
+constexpr int kMaxBlocks = 8192;  // partial sums kept in the workspace
+
+int norm_pass(shampoo_grads* c, float max_norm, float inv_scale, float* out, void* ws, size_t ws_bytes, void* stream,
+              bool clip) {
+  if (!c || !out || !(max_norm > 0.0f) || !(inv_scale > 0.0f) || !std::isfinite(inv_scale)) return SHAMPOO_EINVAL;
+  if (!ws || ws_bytes < c->total) return SHAMPOO_EWORKSPACE;
+  if (ws != c->bound_ws) return SHAMPOO_EINVAL;
+  char* w = static_cast<char*>(ws);
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const auto* table = reinterpret_cast<const dash::GradChunk*>(w + dash::kHeaderBytes);
+  const int n = static_cast<int>(c->chunks.size());
+  const int grid = std::max(1, std::min(n, c->norm_blocks));
+  dash::grad_norm_kernel<<<grid, dash::kListThreads, 0, st>>>(
+      table, n, reinterpret_cast<dash::NormHeader*>(w), reinterpret_cast<double*>(w + c->off_partial), max_norm,
+      inv_scale, out);
+  dash::prof_count_launch();
+  if (cudaGetLastError() != cudaSuccess) return SHAMPOO_ECUDA;
+  if (clip && n > 0) {
+    dash::grad_clip_kernel<<<std::min(n, c->clip_blocks), dash::kListThreads, 0, st>>>(table, n, out);
+    dash::prof_count_launch();
+    if (cudaGetLastError() != cudaSuccess) return SHAMPOO_ECUDA;
+  }
+  return SHAMPOO_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int shampoo_grads_init(shampoo_grads** out, const shampoo_grad* grads, int n_grads, size_t* workspace_bytes) {
+  if (!out || !grads || n_grads < 1 || !workspace_bytes) return SHAMPOO_EINVAL;
+  *out = nullptr;
+  shampoo_grads* c = nullptr;
+  try {
+    c = new shampoo_grads();
+    std::vector<dash::ByteRange> ranges;
+    for (int i = 0; i < n_grads; ++i) {
+      const shampoo_grad& g = grads[i];
+      const bool ok = g.n >= 0 && g.n <= SHAMPOO_MAX_TENSOR && dash::valid_dtype(g.dtype) &&
+                      (g.n == 0 || (g.grad && dash::aligned_to(g.grad, dash::dtype_bytes(g.dtype))));
+      if (!ok) {
+        delete c;
+        return SHAMPOO_EINVAL;
+      }
+      const size_t size = dash::dtype_bytes(g.dtype);
+      dash::add_range(ranges, g.grad, size * static_cast<size_t>(g.n), true);
+      const int flags = g.dtype | (dash::aligned_to(g.grad, 8 * size) ? dash::kVec : 0);
+      for (int64_t at = 0; at < g.n; at += dash::kChunk)
+        c->chunks.push_back({static_cast<char*>(g.grad) + size * static_cast<size_t>(at),
+                             static_cast<int>(std::min<int64_t>(dash::kChunk, g.n - at)), flags});
+    }
+    if (dash::ranges_clash(ranges) || c->chunks.size() > 0x7ffffff) {
+      delete c;
+      return SHAMPOO_EINVAL;
+    }
+  } catch (...) {
+    delete c;
+    return SHAMPOO_EINVAL;
+  }
+  const size_t table = (c->chunks.size() * sizeof(dash::GradChunk) + 255) / 256 * 256;
+  c->off_partial = dash::kHeaderBytes + table;
+  c->total = c->off_partial + kMaxBlocks * sizeof(double);
+  *workspace_bytes = c->total;
+  *out = c;
+  return SHAMPOO_OK;
+}
+
+int shampoo_grads_bind(shampoo_grads* c, void* ws, size_t ws_bytes, void* stream) {
+  if (!c) return SHAMPOO_EINVAL;
+  if (!ws || !dash::aligned_to(ws, 256) || ws_bytes < c->total) return SHAMPOO_EWORKSPACE;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
+  if (cudaStreamIsCapturing(st, &cap) != cudaSuccess) return SHAMPOO_ECUDA;
+  if (cap != cudaStreamCaptureStatusNone) return SHAMPOO_EINVAL;
+  c->bound_ws = nullptr;
+  const int nb = dash::resident_blocks(dash::grad_norm_kernel), cb = dash::resident_blocks(dash::grad_clip_kernel);
+  if (nb < 0 || cb < 0) return SHAMPOO_ECUDA;
+  c->norm_blocks = std::min(nb, kMaxBlocks);
+  c->clip_blocks = cb;
+  if (cudaMemsetAsync(ws, 0, dash::kHeaderBytes, st) != cudaSuccess) return SHAMPOO_ECUDA;
+  if (!c->chunks.empty() &&
+      cudaMemcpyAsync(static_cast<char*>(ws) + dash::kHeaderBytes, c->chunks.data(),
+                      c->chunks.size() * sizeof(dash::GradChunk), cudaMemcpyHostToDevice, st) != cudaSuccess)
+    return SHAMPOO_ECUDA;
+  c->bound_ws = ws;
+  return SHAMPOO_OK;
+}
+
+int shampoo_grad_norm(shampoo_grads* c, float max_norm, float inv_scale, float* out, void* ws, size_t ws_bytes,
+                      void* stream) {
+  return norm_pass(c, max_norm, inv_scale, out, ws, ws_bytes, stream, false);
+}
+
+int shampoo_grad_clip(shampoo_grads* c, float max_norm, float inv_scale, float* out, void* ws, size_t ws_bytes,
+                      void* stream) {
+  return norm_pass(c, max_norm, inv_scale, out, ws, ws_bytes, stream, true);
+}
+
+void shampoo_grads_destroy(shampoo_grads* c) { delete c; }
+
+}  // extern "C"

@@ -1,0 +1,217 @@
+"""Host-side checks of the operators over a list of tensors (no GPU): what
+the C entry points refuse, and the oracle's 8-bit formats and draws."""
+
+import ctypes
+
+import numpy as np
+import pytest
+
+from matrix_inverse_roots_stack_b200 import binding as bd
+from oracle import adamw as oa
+
+
+@pytest.fixture(scope="module")
+def lib():
+    from matrix_inverse_roots_stack_b200 import build
+    build.build()
+    return bd.load()
+
+
+# ---------------------------------------------------------------- gradient lists
+
+def grads_init(lib, rows):
+    arr = (bd.ShampooGrad * max(len(rows), 1))(*[bd.ShampooGrad(*r) for r in rows])
+    ctx, n = ctypes.c_void_p(), ctypes.c_size_t()
+    rc = lib.shampoo_grads_init(ctypes.byref(ctx), arr, len(rows), ctypes.byref(n))
+    return rc, ctx, n.value
+
+
+@pytest.mark.parametrize("rows,ok", [
+    ([(100, 0x1000, bd.DTYPE_F32)], True),
+    ([(100, 0x1002, bd.DTYPE_BF16), (100, 0x10ca, bd.DTYPE_F16)], True),   # adjacent
+    ([(0, None, bd.DTYPE_F32)], True),
+    ([(100, 0x1002, bd.DTYPE_F32)], False),                                # not even its type's alignment
+    ([(100, 0x1001, bd.DTYPE_BF16)], False),
+    ([(100, None, bd.DTYPE_F32)], False),
+    ([(-1, 0x1000, bd.DTYPE_F32)], False),
+    ([((1 << 40) + 1, 0x1000, bd.DTYPE_F32)], False),
+    ([(100, 0x1000, 3)], False),
+    ([(100, 0x1000, bd.DTYPE_F32), (100, 0x1000, bd.DTYPE_F32)], False),   # the same tensor twice
+    ([(100, 0x1000, bd.DTYPE_F32), (100, 0x118c, bd.DTYPE_F32)], False),   # the last element shared
+    ([], False),
+])
+def test_gradient_list(lib, rows, ok):
+    rc, ctx, nbytes = grads_init(lib, rows)
+    assert rc == (bd.SHAMPOO_OK if ok else bd.SHAMPOO_EINVAL)
+    assert (nbytes > 0) == ok and bool(ctx.value) == ok
+    lib.shampoo_grads_destroy(ctx)
+
+
+def test_gradient_calls_validate_before_device_work(lib):
+    rc, ctx, need = grads_init(lib, [(100, 0x1000, bd.DTYPE_F32)])
+    assert rc == 0
+    ws, out = ctypes.c_void_p(0x100000), ctypes.c_void_p(0x2000)
+    assert lib.shampoo_grads_bind(None, ws, need, None) == bd.SHAMPOO_EINVAL
+    assert lib.shampoo_grads_bind(ctx, None, need, None) == bd.SHAMPOO_EWORKSPACE
+    assert lib.shampoo_grads_bind(ctx, ws, need - 1, None) == bd.SHAMPOO_EWORKSPACE
+    assert lib.shampoo_grads_bind(ctx, ctypes.c_void_p(0x100010), need, None) == bd.SHAMPOO_EWORKSPACE
+    for fn in (lib.shampoo_grad_norm, lib.shampoo_grad_clip):
+        assert fn(None, 1.0, 1.0, out, ws, need, None) == bd.SHAMPOO_EINVAL
+        assert fn(ctx, 1.0, 1.0, None, ws, need, None) == bd.SHAMPOO_EINVAL
+        assert fn(ctx, 1.0, 1.0, out, None, need, None) == bd.SHAMPOO_EWORKSPACE
+        assert fn(ctx, 1.0, 1.0, out, ws, need - 1, None) == bd.SHAMPOO_EWORKSPACE
+        assert fn(ctx, 1.0, 1.0, out, ws, need, None) == bd.SHAMPOO_EINVAL  # not bound
+        for max_norm, inv_scale in ((0.0, 1.0), (-1.0, 1.0), (float("nan"), 1.0), (1.0, 0.0), (1.0, -1.0),
+                                    (1.0, float("inf")), (1.0, float("nan"))):
+            assert fn(ctx, max_norm, inv_scale, out, ws, need, None) == bd.SHAMPOO_EINVAL
+    lib.shampoo_grads_destroy(ctx)
+    lib.shampoo_grads_destroy(None)
+
+
+# ---------------------------------------------------------------- AdamW lists
+
+def tensor(base=0x10000, n=1000, **changes):
+    t = dict(n=n, param=base, grad=base + 0x10000, copy=None, m=base + 0x20000, v=base + 0x30000, m_scale=None,
+             v_scale=None, param_dtype=bd.DTYPE_F32, grad_dtype=bd.DTYPE_F32, copy_dtype=bd.DTYPE_F32, state_bits=32,
+             lr_scale=1.0, weight_decay=0.1)
+    if changes.get("state_bits") == 8:
+        t.update(m_scale=base + 0x40000, v_scale=base + 0x41000)
+    t.update(changes)
+    return bd.AdamwTensor(**t)
+
+
+def adamw_init(lib, tensors, **hp):
+    arr = (bd.AdamwTensor * max(len(tensors), 1))(*tensors)
+    ctx, n, elems = ctypes.c_void_p(), ctypes.c_size_t(), ctypes.c_int64(-1)
+    h = bd.make_adamw_hparams(**hp)
+    rc = lib.shampoo_adamw_init(ctypes.byref(ctx), arr, len(tensors), ctypes.byref(h), ctypes.byref(n),
+                                ctypes.byref(elems))
+    return rc, ctx, n.value, elems.value
+
+
+@pytest.mark.parametrize("changes", [
+    {}, {"state_bits": 8}, {"n": 0}, {"n": 0, "param": None, "grad": None, "m": None, "v": None},
+    {"param_dtype": bd.DTYPE_BF16}, {"grad_dtype": bd.DTYPE_F16}, {"copy": 0x70000, "copy_dtype": bd.DTYPE_BF16},
+    {"lr_scale": 0.0}, {"weight_decay": 0.0}, {"param": 0x10004},
+    {"state_bits": 8, "m": 0x30001, "v": 0x40003, "m_scale": 0x50007}])
+def test_adamw_list_accepts(lib, changes):
+    rc, ctx, nbytes, elems = adamw_init(lib, [tensor(**changes)])
+    assert rc == bd.SHAMPOO_OK and nbytes > 0
+    assert elems == -(-changes.get("n", 1000) // bd.QBLOCK) * bd.QBLOCK
+    lib.shampoo_adamw_destroy(ctx)
+
+
+@pytest.mark.parametrize("changes", [
+    {"n": -1}, {"n": (1 << 40) + 1}, {"param": None}, {"grad": None}, {"m": None}, {"v": None},
+    {"param_dtype": bd.DTYPE_F16}, {"param_dtype": 5}, {"grad_dtype": -1}, {"state_bits": 16}, {"state_bits": 4},
+    {"state_bits": 8, "m_scale": None}, {"state_bits": 8, "v_scale": None},
+    {"copy": 0x70000, "copy_dtype": bd.DTYPE_F32},
+    {"copy": 0x70000, "copy_dtype": bd.DTYPE_BF16, "param_dtype": bd.DTYPE_BF16},
+    {"copy": 0x70001, "copy_dtype": bd.DTYPE_BF16}, {"param": 0x10002}, {"grad": 0x20001}, {"m": 0x30002},
+    {"lr_scale": -1.0}, {"lr_scale": float("nan")}, {"weight_decay": -0.1}, {"weight_decay": float("inf")},
+    {"grad": 0x10000}, {"m": 0x10000}, {"v": 0x30000 + 3996}, {"copy": 0x10000, "copy_dtype": bd.DTYPE_BF16},
+    {"state_bits": 8, "v_scale": 0x50003}])  # four blocks of scales at 0x50000
+def test_adamw_list_refuses(lib, changes):
+    rc, ctx, nbytes, _ = adamw_init(lib, [tensor(**changes)])
+    assert rc == bd.SHAMPOO_EINVAL and not ctx.value
+
+
+def test_adamw_list_refuses_shared_parameters(lib):
+    assert adamw_init(lib, [])[0] == bd.SHAMPOO_EINVAL
+    assert adamw_init(lib, [tensor(), tensor()])[0] == bd.SHAMPOO_EINVAL
+    two = [tensor(), tensor(0x80000)]
+    rc, ctx, _, elems = adamw_init(lib, two)
+    assert rc == bd.SHAMPOO_OK and elems == 2048
+    lib.shampoo_adamw_destroy(ctx)
+    # a gradient may be shared (it is only read), but is no other's parameter
+    rc, ctx, _, _ = adamw_init(lib, [tensor(), tensor(0x80000, grad=0x20000)])
+    assert rc == bd.SHAMPOO_OK
+    lib.shampoo_adamw_destroy(ctx)
+    assert adamw_init(lib, [tensor(), tensor(0x80000, grad=0x10000)])[0] == bd.SHAMPOO_EINVAL
+
+
+@pytest.mark.parametrize("hp", [{"beta1": 1.0}, {"beta1": -0.1}, {"beta2": 1.0}, {"beta2": float("nan")},
+                                {"adam_eps": 0.0}, {"adam_eps": 1e-40}, {"adam_eps": float("inf")}])
+def test_adamw_hparams(lib, hp):
+    assert adamw_init(lib, [tensor()], **hp)[0] == bd.SHAMPOO_EINVAL
+
+
+def test_adamw_calls_validate_before_device_work(lib):
+    rc, ctx, need, _ = adamw_init(lib, [tensor()])
+    assert rc == 0
+    ws, p = ctypes.c_void_p(0x100000), ctypes.c_void_p(0x2000)
+    assert lib.shampoo_adamw_bind(None, 0, ws, need, None) == bd.SHAMPOO_EINVAL
+    assert lib.shampoo_adamw_bind(ctx, -1, ws, need, None) == bd.SHAMPOO_EINVAL
+    assert lib.shampoo_adamw_bind(ctx, 0, None, need, None) == bd.SHAMPOO_EWORKSPACE
+    assert lib.shampoo_adamw_bind(ctx, 0, ws, need - 1, None) == bd.SHAMPOO_EWORKSPACE
+    assert lib.shampoo_adamw_bind(ctx, 0, ctypes.c_void_p(0x100080), need, None) == bd.SHAMPOO_EWORKSPACE
+    calls = [lambda w, n: lib.shampoo_adamw_step(ctx, 0, 1e-3, None, None, w, n, None),
+             lambda w, n: lib.shampoo_adamw_load_moments(ctx, p, p, w, n, None),
+             lambda w, n: lib.shampoo_adamw_read_moments(ctx, p, p, bd.DTYPE_F32, w, n, None),
+             lambda w, n: lib.shampoo_adamw_steps_taken(ctx, w, n, None, ctypes.byref(ctypes.c_int()))]
+    for call in calls:
+        assert call(None, need) == bd.SHAMPOO_EWORKSPACE
+        assert call(ws, need - 1) == bd.SHAMPOO_EWORKSPACE
+        assert call(ws, need) == bd.SHAMPOO_EINVAL  # not bound
+    assert lib.shampoo_adamw_step(None, 0, 1e-3, None, None, ws, need, None) == bd.SHAMPOO_EINVAL
+    lib.shampoo_adamw_destroy(ctx)
+    lib.shampoo_adamw_destroy(None)
+
+
+def test_header_constants(lib):
+    text = open(lib._name.replace("matrix_inverse_roots_stack_b200/libdash_b200.so", "include/dash_b200.h")).read()
+    for name, value in (("DTYPE_F32", bd.DTYPE_F32), ("DTYPE_BF16", bd.DTYPE_BF16), ("DTYPE_F16", bd.DTYPE_F16),
+                        ("QBLOCK", bd.QBLOCK)):
+        assert f"#define SHAMPOO_{name} {value}" in text
+    assert oa.BLOCK == bd.QBLOCK
+
+
+@pytest.mark.parametrize("make", [
+    lambda t: bd.GradClip([]), lambda t: bd.GradClip([t.zeros(4)]),
+    lambda t: bd.AdamW([], []), lambda t: bd.AdamW([t.zeros(4)], [t.zeros(4)])])
+def test_binding_refuses_lists_without_cuda_tensors(lib, make):
+    with pytest.raises(ValueError):
+        make(pytest.importorskip("torch"))
+
+
+# ---------------------------------------------------------------- the oracle's formats
+
+@pytest.mark.parametrize("fmt", [oa.M_FORMAT, oa.V_FORMAT])
+def test_every_code_is_held_exactly(fmt):
+    bits = 128 if fmt is oa.M_FORMAT else 256
+    codes = np.arange(bits - (fmt is oa.M_FORMAT))  # 0x7f is not a number of e4m3
+    x = oa.decode(codes, np.full(1, 127), fmt)
+    assert np.all(np.diff(x) > 0) and x[0] == 0 and x[-1] == fmt[2]
+    assert oa.block_exponents(x, fmt) == [0]
+    for u in (None, np.zeros(len(x), int), np.full(len(x), 65535)):
+        assert np.array_equal(oa.held(x, fmt, [0], u), x)
+    assert oa.block_exponents(x * 2.0 ** -30, fmt) == [-30]
+    assert oa.block_exponents([fmt[2] * (1 + 2.0 ** -30)], fmt) == [1]
+
+
+def test_e4m3_is_torchs():
+    torch = pytest.importorskip("torch")
+    codes = np.array([c for c in range(256) if c & 127 != 127], dtype=np.uint8)
+    ref = torch.from_numpy(codes).view(torch.float8_e4m3fn).float().numpy()
+    assert np.array_equal(oa.decode(codes, np.full(1, 127), oa.M_FORMAT), ref)
+
+
+def test_draws_are_uniform_and_independent():
+    # each statistic is a mean of n products of independent unit-variance
+    # variables, about N(0, 1/n); 6 sigma over the few hundred looks below
+    n = 1 << 18
+    i = np.arange(n) + (1 << 32) - n // 2
+    prev = None
+    for t in range(1, 9):
+        d = [(x.astype(np.float64) + 0.5) / 65536 - 0.5 for x in oa.draws(12345678901, t, 3, i)]
+        d = [x * np.sqrt(12) for x in d]
+        looks = [x for x in d] + [d[0] * d[1], d[0] * d[2], d[1] * d[2]]
+        for lag in (1, 2, 8, 32, 256, 2048):
+            looks += [x[:-lag] * x[lag:] for x in d]
+        if prev is not None:
+            looks += [a * b for a, b in zip(d, prev)]
+        prev = d
+        for x in looks:
+            assert abs(x.mean()) * np.sqrt(len(x)) < 6
+    assert not np.array_equal(oa.draws(1, 1, 0, i)[0], oa.draws(1, 1, 1, i)[0])
+    assert not np.array_equal(oa.draws(1, 1, 0, i)[0], oa.draws(1 + (1 << 32), 1, 0, i)[0])
