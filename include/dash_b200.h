@@ -335,7 +335,7 @@ SHAMPOO_API void shampoo_destroy(shampoo_ctx* ctx);
 #define SHAMPOO_DTYPE_F16 2
 
 #define SHAMPOO_QBLOCK 256                  /* elements that share a scale in 8-bit moments */
-#define SHAMPOO_MAX_TENSOR (1ll << 40)      /* elements of one tensor, at most */
+#define SHAMPOO_MAX_TENSOR (1ll << 38)      /* elements of one tensor, at most; a list holds under 2^39 */
 
 typedef struct shampoo_grads shampoo_grads;
 
@@ -407,7 +407,7 @@ typedef struct {
 
 typedef struct {
   float beta1, beta2;
-  float adam_eps; /* at least FLT_MIN */
+  float adam_eps; /* at least 1e-30 */
   uint64_t seed;  /* of the rounding draws */
 } shampoo_adamw_hparams;
 
@@ -429,7 +429,8 @@ SHAMPOO_API int shampoo_adamw_bind(shampoo_adamw* ctx, int steps_taken, void* ws
 /* One AdamW step t of the whole list, in one launch; per element, in fp32:
  *   g = coef grad;  m <- beta1 m + (1 - beta1) g;  v <- beta2 v + (1 - beta2) g^2;
  *   param -= lr lr_scale ( m_hat / (sqrt(v_hat) + adam_eps) + weight_decay param ),
- *   m_hat = m / (1 - beta1^t),  v_hat = v / (1 - beta2^t).
+ *   m_hat = m / (1 - beta1^t),  v_hat = v / (1 - beta2^t)
+ * (a v below fp32's normal range counts as 0 in the root).
  * 8-bit moments enter as the values they stand for; the update uses the new
  * moments before they are rounded.  Moments in 8 bits and bf16 parameters are
  * rounded stochastically: x lies between two neighbours of its format and

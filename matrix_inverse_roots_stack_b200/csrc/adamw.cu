@@ -2,19 +2,97 @@
 // and the 8-bit moments' way in and out (include/dash_b200.h has the
 // formulas and the formats).
 //
-// All of it streams through HBM once.  Each warp takes 256 consecutive
-// elements at a time, eight to a lane, so that every access of an aligned
-// tensor is 8 to 32 bytes a lane and a block of 8-bit moments belongs to one
-// warp: its maximum is two warp reductions and never leaves registers.
+// All of it streams through HBM once.  A warp takes a block of 256
+// consecutive elements at a time, eight to a lane, so that a block of 8-bit
+// moments belongs to one warp: its maximum is one warp reduction and never
+// leaves registers.  HBM is the bound with 32-bit moments (28 bytes an
+// element); with 8-bit ones (10 to 16 bytes) the instructions count as much:
+// at the copy rate an SM has about 55 issue slots for an element of 10 bytes.
+// Hence products and sums two at a time (f32x2), codes that are cut out of
+// fp32 bit patterns instead of converted, three-operand maxima, and loads
+// that are taken off the warps that compute (adamw_step).
 //
-// The moments are computed with every product and sum rounded on its own (no
-// contraction), so that their 8-bit codes do not depend on how a compiler
-// fuses them.
+// The moments' products and sums are rounded one by one (no contraction), so
+// that their 8-bit codes do not depend on how a compiler fuses them.
+#include <atomic>
+
 #include "adamw.cuh"
+#include "launch_util.cuh"
 #include "profile.cuh"
 
 namespace dash {
 namespace {
+
+// ---------------------------------------------------------------- two fp32 numbers at a time
+
+typedef unsigned long long f32x2;
+
+__device__ __forceinline__ f32x2 pack2(float a, float b) {
+  f32x2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ f32x2 both(float a) { return pack2(a, a); }
+__device__ __forceinline__ float low(f32x2 a) { return __uint_as_float(static_cast<unsigned>(a)); }
+__device__ __forceinline__ float high(f32x2 a) { return __uint_as_float(static_cast<unsigned>(a >> 32)); }
+__device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b) {
+  f32x2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ f32x2 add2(f32x2 a, f32x2 b) {
+  f32x2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
+  f32x2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+// Square roots of v >= 0, and a reciprocal within 2^-23 whose operand is
+// normal, as the smallest adam_eps sees to.
+//
+// root: within 2^-23; below fp32's normal range v counts as 0.
+// root2: rounded to nearest, but for about one number in a million, by
+// Markstein's correction of an approximation (P. Markstein, "Computation of
+// elementary functions on the IBM RISC System/6000 processor", 1990): with y
+// near 1 / sqrt(v) and s = v y, the remainder v - s^2 is exact in a fused
+// product, and s + (v - s^2) y / 2 is off by the product of two errors before
+// it is rounded.  8-bit moments take this one: their codes then are those of
+// the correctly rounded root.  (The operand's floor keeps v = 0 at 0; below
+// the normal range the root comes out smaller.)
+__device__ __forceinline__ float root(float v) {
+  float r;
+  asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+  return r;
+}
+__device__ __forceinline__ float inverse_root(float v) {
+  float r;
+  asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(fmaxf(v, 0x1p-126f)));
+  return r;
+}
+__device__ __forceinline__ f32x2 root2(f32x2 v) {
+  const f32x2 y = pack2(inverse_root(low(v)), inverse_root(high(v)));
+  const f32x2 s = mul2(v, y);
+  return fma2(fma2(s ^ 0x8000000080000000ull, s, v), mul2(y, both(0.5f)), s);
+}
+__device__ __forceinline__ float reciprocal(float x) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+// max(a, |b|, |c|), NaN when one of them is.
+__device__ __forceinline__ float max_abs3(float a, float b, float c) {
+  float r;
+  asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+__device__ __forceinline__ float warp_max(float x) {
+  float r;
+  asm volatile("redux.sync.max.abs.NaN.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(x));
+  return r;
+}
 
 // ---------------------------------------------------------------- rounding draws
 //
@@ -33,9 +111,10 @@ __device__ __forceinline__ unsigned key_word(unsigned x, unsigned w) {
   x ^= x >> 15;
   return x + kWeyl;
 }
-// key: of the seed, step, tensor and the high half of the element's index.
-__device__ __forceinline__ unsigned draw_bits(unsigned key, unsigned elem) {
-  unsigned x = elem * kWeyl + key;
+// x: the element's index (low half) times kWeyl, plus a key of the seed, the
+// step, the tensor and the index's high half.  The upper 16 bits round m, the
+// lower 16 v.
+__device__ __forceinline__ unsigned draw_bits(unsigned x) {
   x ^= x >> 16;
   x *= kMulA;
   x ^= x >> 15;
@@ -51,485 +130,947 @@ __device__ __forceinline__ unsigned draw_bits(unsigned key, unsigned elem) {
 // fp32's gradual underflow is the format's, and the code is the top of the
 // bit pattern, rounded by what is added below it.
 constexpr float kM8Down = 0x1p-120f, kV8Down = 0x1p-126f;
-
-__device__ __forceinline__ float power_of_two(int i) { return __int_as_float(i << 23); }  // 2^(i-127), 1 <= i <= 254
+constexpr int kM8Shift = 4, kV8Shift = 5;  // bring the code into the pattern's top byte
 
 // Scale byte i of a block, standing for 2^(i - 127): the smallest that brings
 // the block's maximum within the format (448 = 1.75 2^8, 31744 = 1.9375
-// 2^14).  255: the maximum is not finite, and the block reads back so.
-__device__ __forceinline__ int m8_scale(unsigned amax) {
-  return amax >= 0x7f800000u ? 255 : max(1, static_cast<int>((amax + 0x1fffffu) >> 23) - 8);
-}
-__device__ __forceinline__ int v8_scale(unsigned amax) {
-  return amax >= 0x7f800000u ? 255 : max(1, static_cast<int>((amax + 0x07ffffu) >> 23) - 14);
-}
-// What to multiply an element of the block by: 1 / scale (0 for a scale that
-// is not finite, whose codes do not matter).
-__device__ __forceinline__ float inverse_scale(int i) { return i == 255 ? 0.0f : power_of_two(254 - i); }
-
-// Code of a magnitude that 'unit' = inverse_scale brings into range; u: 16
-// random bits (rounded up where the dropped part and they reach a whole).
-__device__ __forceinline__ unsigned m8_code(float y, float unit, unsigned u) {
-  const float x = __fmul_rn(__fmul_rn(fabsf(y), unit), kM8Down);
-  return ((__float_as_uint(x) + (u << 4)) >> 20) | ((__float_as_uint(y) >> 24) & 0x80u);
-}
-// r > 0 is never stored as 0: beside a nonzero first moment a vanished
-// second one would make the next update explode.
-__device__ __forceinline__ unsigned v8_code(float r, float unit, unsigned u) {
-  const float x = __fmul_rn(__fmul_rn(r, unit), kV8Down);
-  return max((__float_as_uint(x) + (u << 3)) >> 19, r > 0.0f ? 1u : 0u);
-}
-__device__ __forceinline__ unsigned nearest_even(unsigned b, int low) {
-  return (b + ((1u << (low - 1)) - 1u) + ((b >> low) & 1u)) >> low;
-}
-__device__ __forceinline__ unsigned m8_nearest(float y, float unit) {
-  const float x = __fmul_rn(__fmul_rn(fabsf(y), unit), kM8Down);
-  return nearest_even(__float_as_uint(x), 20) | ((__float_as_uint(y) >> 24) & 0x80u);
-}
-__device__ __forceinline__ unsigned v8_nearest(float r, float unit) {
-  const float x = __fmul_rn(__fmul_rn(r, unit), kV8Down);
-  return max(nearest_even(__float_as_uint(x), 19), r > 0.0f ? 1u : 0u);
-}
-
-// Two codes at a time are the bits of fp16 numbers: e4m3 and e4m4 lie inside
-// e5m10 up to the exponent's bias, 2^8 and 2^14, which goes into the
-// block's factor.
-__device__ __forceinline__ float m8_factor(int i) {
-  return i == 0 ? 0.0f : i == 255 ? __int_as_float(0x7f800000) : power_of_two(i + 8);
-}
-__device__ __forceinline__ float v8_factor(int i) {
-  return i == 0 ? 0.0f : i == 255 ? __int_as_float(0x7f800000) : power_of_two(i + 14);
-}
-__device__ __forceinline__ void m8_values4(unsigned codes, float factor, float* m) {
-#pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    unsigned w = __byte_perm(codes, 0, h ? 0x3424 : 0x1404);  // codes in the high bytes of the halves
-    w = (w & 0x80008000u) | ((w & 0x7f007f00u) >> 1);
-    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w));
-    m[2 * h] = __fmul_rn(f.x, factor);
-    m[2 * h + 1] = __fmul_rn(f.y, factor);
+// 2^14).  255: the maximum is not finite, and the block reads back so,
+// whatever its codes.  What is kept of the scale is the exponent field of a
+// float: (i + 8) << 23 or (i + 14) << 23.
+__device__ __forceinline__ unsigned bits_of(float x) { return __float_as_uint(x); }
+__device__ __forceinline__ float float_of(unsigned b) { return __uint_as_float(b); }
+template <int kTop, unsigned kSlack>
+struct BlockScale {
+  unsigned e;
+  __device__ __forceinline__ explicit BlockScale(float amax)
+      : e(max((bits_of(amax) + kSlack) & 0xff800000u, (kTop + 1u) << 23)) {}
+  // 1 / scale (of no use where the maximum is not finite)
+  __device__ __forceinline__ float inverse() const { return float_of(((254u + kTop) << 23) - e); }
+  __device__ __forceinline__ uint8_t byte(float amax) const {
+    return static_cast<uint8_t>(not_finite(amax) ? 255u : (e >> 23) - kTop);
   }
-}
-__device__ __forceinline__ void v8_values4(unsigned codes, float factor, float* r) {
-#pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    const unsigned w = __byte_perm(codes, 0, h ? 0x4342 : 0x4140) << 6;
-    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w));
-    r[2 * h] = __fmul_rn(f.x, factor);
-    r[2 * h + 1] = __fmul_rn(f.y, factor);
-  }
-}
-__device__ __forceinline__ unsigned pack4(const unsigned* c) {
-  return c[0] | (c[1] << 8) | (c[2] << 16) | (c[3] << 24);
-}
-
-// bf16 pattern of a parameter, rounded by 16 random bits: where parameters
-// have no fp32 master, rounding to nearest would drop every update below half
-// a bf16 step (2^-9 of the value).
-__device__ __forceinline__ unsigned bf16_bits(float p, unsigned draw) {
-  const unsigned b = __float_as_uint(p);
-  if (not_finite(p)) return (b >> 16) | ((b & 0x7fffffu) ? 0x40u : 0u);
-  return (b + ((draw * kMulC) >> 16)) >> 16;
-}
-
-struct Coefs {
-  float beta1, beta2, om1, om2, eps, c1, c2, lr, decay, coef;
 };
+typedef BlockScale<8, 0x1fffffu> M8Scale;
+typedef BlockScale<14, 0x07ffffu> V8Scale;
 
-// One element: moments, then the parameter.  Returns what the caller flags
-// as not finite, as bits of magnitudes.
-__device__ __forceinline__ void moments(const Coefs& k, float grad, float& m, float& v) {
-  const float g = __fmul_rn(grad, k.coef);
-  m = __fadd_rn(__fmul_rn(m, k.beta1), __fmul_rn(g, k.om1));
-  v = __fadd_rn(__fmul_rn(v, k.beta2), __fmul_rn(__fmul_rn(g, k.om2), g));
+// Code in the top byte.  x: bits of the scaled magnitude (or signed number),
+// as above; y: the number itself; u: 16 random bits in bytes 1 and 2, so that
+// x is rounded up where the dropped part and they reach a whole.
+__device__ __forceinline__ unsigned m8_code(unsigned x, float y, unsigned u) {
+  const unsigned c = (x << kM8Shift) + u;  // the sign is shifted out
+  return (c & 0x7fffffffu) | (__float_as_uint(y) & 0x80000000u);
 }
-__device__ __forceinline__ float updated(const Coefs& k, float p, float m, float r) {
-  return p - k.lr * (__fdividef(m * k.c1, fmaf(r, k.c2, k.eps)) + k.decay * p);
-}
-__device__ __forceinline__ unsigned magnitude(float x) { return __float_as_uint(x) & 0x7fffffffu; }
-
-// ---------------------------------------------------------------- 32-bit moments
-
-__device__ __forceinline__ unsigned step32(const AdamwChunk& c, const Coefs& k, unsigned key) {
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int pt = (c.flags >> kParamShift) & 15, gt = (c.flags >> kGradShift) & 15, ct = (c.flags >> kCopyShift) & 15;
-  const unsigned elem = static_cast<unsigned>(c.elem);
-  unsigned worst = 0;
-  for (int b = warp * kQBlock; b < c.count; b += kListWarps * kQBlock) {
-    if ((c.flags & kFlagVec) && b + kQBlock <= c.count) {
-      const int i = (b >> 3) + lane;
-      Raw8 rp, rg, rm, rv;
-      load8(c.grad, i, gt, rg);
-      load32B(static_cast<const float*>(c.m) + 8 * i, rm.w);
-      load32B(static_cast<const float*>(c.v) + 8 * i, rv.w);
-      load8(c.param, i, pt, rp);
-      float p[8], g[8], m[8], v[8];
-      widen8(rg, gt, g);
-      widen8(rp, pt, p);
+__device__ __forceinline__ unsigned v8_code(unsigned x, unsigned u) { return (x << kV8Shift) + u; }
+// r > 0 is never stored as 0: beside a nonzero first moment a vanished
+// second one would make the next update explode.  Four codes in one word:
+// whether one is 0, and the codes with 1 in its place where r > 0.
+__device__ __forceinline__ unsigned zero_bytes(unsigned w) { return (w - 0x01010101u) & ~w & 0x80808080u; }
+__device__ __forceinline__ unsigned v8_floor(unsigned w, const f32x2* r) {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        m[j] = __uint_as_float(rm.w[j]);
-        v[j] = __uint_as_float(rv.w[j]);
-        moments(k, g[j], m[j], v[j]);
-        p[j] = updated(k, p[j], m[j], __fsqrt_rn(v[j]));
-        worst = max(worst, max(magnitude(m[j]), max(magnitude(v[j]), magnitude(p[j]))));
-      }
-      store8(c.m, i, SHAMPOO_DTYPE_F32, m);
-      store8(c.v, i, SHAMPOO_DTYPE_F32, v);
-      if (pt == SHAMPOO_DTYPE_F32) {
-        store8(c.param, i, SHAMPOO_DTYPE_F32, p);
-        if (c.copy) store8(c.copy, i, ct, p);
-      } else {
-        unsigned w[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-          w[j] = bf16_bits(p[2 * j], draw_bits(key, elem + 8 * i + 2 * j)) |
-                 (bf16_bits(p[2 * j + 1], draw_bits(key, elem + 8 * i + 2 * j + 1)) << 16);
-        *(static_cast<uint4*>(c.param) + i) = make_uint4(w[0], w[1], w[2], w[3]);
-      }
-    } else {
-      for (int i = b + lane; i < min(b + kQBlock, c.count); i += 32) {
-        float m = static_cast<const float*>(c.m)[i], v = static_cast<const float*>(c.v)[i];
-        moments(k, load1(c.grad, i, gt), m, v);
-        const float p = updated(k, load1(c.param, i, pt), m, __fsqrt_rn(v));
-        worst = max(worst, max(magnitude(m), max(magnitude(v), magnitude(p))));
-        static_cast<float*>(c.m)[i] = m;
-        static_cast<float*>(c.v)[i] = v;
-        if (pt == SHAMPOO_DTYPE_F32) {
-          static_cast<float*>(c.param)[i] = p;
-          if (c.copy) store1(c.copy, i, ct, p);
-        } else {
-          static_cast<unsigned short*>(c.param)[i] = bf16_bits(p, draw_bits(key, elem + i));
-        }
-      }
-    }
+  for (int j = 0; j < 4; ++j) {
+    const float x = j & 1 ? high(r[j / 2]) : low(r[j / 2]);
+    if (x > 0.0f && !(w & (0xffu << (8 * j)))) w |= 1u << (8 * j);
   }
-  return worst;
+  return w;
+}
+__device__ __forceinline__ unsigned top_bytes(unsigned a, unsigned b, unsigned c, unsigned d) {
+  return __byte_perm(__byte_perm(a, b, 0x0073), __byte_perm(c, d, 0x0073), 0x5410);
+}
+// To nearest, ties to even: what to add for that.
+__device__ __forceinline__ unsigned nearest_even(unsigned x, int shift) {
+  return 0x7fffffu + ((x >> (24 - shift)) & 1u);
 }
 
-// ---------------------------------------------------------------- 8-bit moments
-
-__device__ __forceinline__ unsigned step8(const AdamwChunk& c, const Coefs& k, unsigned key) {
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int pt = (c.flags >> kParamShift) & 15, gt = (c.flags >> kGradShift) & 15, ct = (c.flags >> kCopyShift) & 15;
-  const unsigned elem = static_cast<unsigned>(c.elem);
-  unsigned worst = 0;
-  for (int b = warp * kQBlock; b < c.count; b += kListWarps * kQBlock) {
-    const bool vec = (c.flags & kFlagVec) && b + kQBlock <= c.count;
-    uint8_t* ms = c.m_scale + (b >> 8);
-    uint8_t* vs = c.v_scale + (b >> 8);
-    const int i0 = vec ? b + 8 * lane : b + lane;  // this lane's elements: i0 + j, or i0 + 32 j
-    const int stride = vec ? 1 : 32;
-    float p[8], m[8], r[8];
-    unsigned mmax = 0, rmax = 0;
-    {
-      float g[8];
-      unsigned cm[2], cv[2];
-      const float mf = m8_factor(*ms), vf = v8_factor(*vs);
-      if (vec) {
-        Raw8 rp, rg;
-        load8(c.grad, i0 >> 3, gt, rg);
-        load8(c.param, i0 >> 3, pt, rp);
-        const uint2 qm = *reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(c.m) + i0);
-        const uint2 qv = *reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(c.v) + i0);
-        cm[0] = qm.x, cm[1] = qm.y, cv[0] = qv.x, cv[1] = qv.y;
-        widen8(rg, gt, g);
-        widen8(rp, pt, p);
-      } else {
-        cm[0] = cm[1] = cv[0] = cv[1] = 0;
+// Decoding goes through fp16, two codes at a time: there is an instruction
+// for e4m3, and e4m4 lies inside e5m10 up to the exponent's bias, 2^14, which
+// goes into the block's factor.  (A block of zeros that no kernel has written
+// has scale 0 and codes 0.)
+__device__ __forceinline__ float m8_factor(int i) { return __int_as_float(i << 23); }  // infinite for 255
+__device__ __forceinline__ float v8_factor(int i) { return __int_as_float(i << 23) * 0x1p14f; }
+__device__ __forceinline__ f32x2 from_half2(unsigned w) {
+  const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w));
+  return pack2(f.x, f.y);
+}
+__device__ __forceinline__ void m8_values4(unsigned codes, f32x2 factor, f32x2* m) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const int i = i0 + 32 * j;
-          const bool in = i < c.count;
-          g[j] = in ? load1(c.grad, i, gt) : 0.0f;
-          p[j] = in ? load1(c.param, i, pt) : 0.0f;
-          if (in) {
-            cm[j >> 2] |= static_cast<unsigned>(static_cast<const uint8_t*>(c.m)[i]) << (8 * (j & 3));
-            cv[j >> 2] |= static_cast<unsigned>(static_cast<const uint8_t*>(c.v)[i]) << (8 * (j & 3));
-          }
-        }
-      }
-      m8_values4(cm[0], mf, m);
-      m8_values4(cm[1], mf, m + 4);
-      v8_values4(cv[0], vf, r);
-      v8_values4(cv[1], vf, r + 4);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        float v = __fmul_rn(r[j], r[j]);
-        moments(k, g[j], m[j], v);
-        r[j] = __fsqrt_rn(v);
-        p[j] = updated(k, p[j], m[j], r[j]);
-        if (!vec && i0 + 32 * j >= c.count) m[j] = r[j] = p[j] = 0.0f;
-        mmax = max(mmax, magnitude(m[j]));
-        rmax = max(rmax, magnitude(r[j]));
-        worst = max(worst, magnitude(p[j]));
-      }
-    }
-    worst = max(worst, max(mmax, rmax));
-    mmax = __reduce_max_sync(0xffffffffu, mmax);
-    rmax = __reduce_max_sync(0xffffffffu, rmax);
-    const int mi = m8_scale(mmax), vi = v8_scale(rmax);
-    const float mu = inverse_scale(mi), vu = inverse_scale(vi);
-    unsigned cm[8], cv[8], h[8];
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      h[j] = draw_bits(key, elem + i0 + stride * j);
-      cm[j] = m8_code(m[j], mu, h[j] >> 16);
-      cv[j] = v8_code(r[j], vu, h[j] & 0xffffu);
-    }
-    if (lane == 0) {
-      *ms = static_cast<uint8_t>(mi);
-      *vs = static_cast<uint8_t>(vi);
-    }
-    if (vec) {
-      *reinterpret_cast<uint2*>(static_cast<uint8_t*>(c.m) + i0) = make_uint2(pack4(cm), pack4(cm + 4));
-      *reinterpret_cast<uint2*>(static_cast<uint8_t*>(c.v) + i0) = make_uint2(pack4(cv), pack4(cv + 4));
-      if (pt == SHAMPOO_DTYPE_F32) {
-        store8(c.param, i0 >> 3, SHAMPOO_DTYPE_F32, p);
-        if (c.copy) store8(c.copy, i0 >> 3, ct, p);
-      } else {
-        unsigned w[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) w[j] = bf16_bits(p[2 * j], h[2 * j]) | (bf16_bits(p[2 * j + 1], h[2 * j + 1]) << 16);
-        *(static_cast<uint4*>(c.param) + (i0 >> 3)) = make_uint4(w[0], w[1], w[2], w[3]);
-      }
-    } else {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const int i = i0 + 32 * j;
-        if (i >= c.count) continue;
-        static_cast<uint8_t*>(c.m)[i] = static_cast<uint8_t>(cm[j]);
-        static_cast<uint8_t*>(c.v)[i] = static_cast<uint8_t>(cv[j]);
-        if (pt == SHAMPOO_DTYPE_F32) {
-          static_cast<float*>(c.param)[i] = p[j];
-          if (c.copy) store1(c.copy, i, ct, p[j]);
-        } else {
-          static_cast<unsigned short*>(c.param)[i] = bf16_bits(p[j], h[j]);
-        }
-      }
-    }
+  for (int h = 0; h < 2; ++h) {
+    unsigned w;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(w) : "h"(static_cast<unsigned short>(codes >> (16 * h))));
+    m[h] = mul2(from_half2(w), factor);
   }
-  return worst;
+}
+__device__ __forceinline__ void v8_values4(unsigned codes, f32x2 factor, f32x2* r) {
+#pragma unroll
+  for (int h = 0; h < 2; ++h)
+    r[h] = mul2(from_half2(__byte_perm(codes, 0, h ? 0x4342 : 0x4140) << 6), factor);
+}
+
+// ---------------------------------------------------------------- the list's blocks
+
+// The tensor that unit 'b' (a block or tile) belongs to, at or behind tensor
+// 'at': 'first' holds the n tensors' first units.  Whole warp, 32 tensors at
+// a time.
+__device__ __forceinline__ int find_tensor(const int* first, int n, int b, int at) {
+  const int lane = threadIdx.x & 31;
+  for (;;) {
+    const int k = at + 1 + lane;
+    const int c = __popc(__ballot_sync(0xffffffffu, k < n && __ldg(first + k) <= b));
+    at += c;
+    if (c < 32) return at;
+  }
+}
+
+// The same from anywhere in the list: the search narrows 32 ways at a time.
+__device__ __forceinline__ int first_tensor(const int* first, int n, int b) {
+  const int lane = threadIdx.x & 31;
+  int at = 0, span = n;
+  while (span > 32) {
+    const int step = (span + 31) / 32, k = at + lane * step;
+    const int c = __popc(__ballot_sync(0xffffffffu, lane * step < span && __ldg(first + k) <= b));
+    at += max(c - 1, 0) * step;
+    span = min(step, n - at);
+  }
+  return find_tensor(first, n, b, at);
 }
 
 // ---------------------------------------------------------------- the step
 
-// Which: 0 every tensor has 32-bit moments, 1 every tensor has 8-bit ones, 2
-// both occur.
-template <int Which>
-__global__ void __launch_bounds__(kListThreads) adamw_step_kernel(const AdamwChunk* __restrict__ chunks, int n_chunks,
-                                                                  AdamwHeader* hdr, const AdamwArgs a) {
-  Coefs k;
-  k.coef = a.coef ? *a.coef : 1.0f;
-  k.beta1 = a.beta1;
-  k.beta2 = a.beta2;
-  k.om1 = 1.0f - a.beta1;
-  k.om2 = 1.0f - a.beta2;
-  k.eps = a.eps;
-  k.c1 = a.step ? a.c1 : hdr->c1;
-  k.c2 = a.step ? a.c2 : hdr->c2;
-  const int t = a.step ? a.step : hdr->t + 1;
-  const float lr = a.lr_device ? *a.lr_device : a.lr;
-  const bool skip = not_finite(k.coef);  // non-finite gradients: the step is not taken
-  const unsigned base = key_word(key_word(key_word(0u, a.seed_lo), a.seed_hi), static_cast<unsigned>(t));
-  unsigned worst = 0;
-  if (!skip) {
-    for (int i = blockIdx.x; i < n_chunks; i += gridDim.x) {
-      const AdamwChunk c = chunks[i];
-      k.lr = lr * c.lr_scale;
-      k.decay = c.decay;
-      const unsigned key =
-          key_word(key_word(base, static_cast<unsigned>(c.tensor)), static_cast<unsigned>(c.elem >> 32));
-      const bool eight = Which == 1 || (Which == 2 && (c.flags & kFlagEight));
-      worst = max(worst, eight ? step8(c, k, key) : step32(c, k, key));
+// Scalars of a step that are not launch arguments.
+struct Coefs {
+  float coef, d1, d0, lr;
+};
+__device__ __forceinline__ f32x2 pair(float2 a) { return pack2(a.x, a.y); }
+
+// bf16 pattern of a parameter, rounded by 16 random bits: where parameters
+// have no fp32 master, rounding to nearest would drop every update below half
+// a bf16 step (2^-9 of the value).
+__device__ __forceinline__ unsigned bf16_up(float p, unsigned draw) {
+  return __float_as_uint(p) + ((draw * kMulC) >> 16);  // its upper half
+}
+__device__ __forceinline__ unsigned bf16_not_finite(float p) {  // the upper half, a NaN kept one
+  const unsigned b = __float_as_uint(p);
+  return (b & 0x7fffffffu) > 0x7f800000u ? b | 0x400000u : b;
+}
+
+// Where a tile of a tensor lies: every pointer at its first element.
+struct TileDesc {
+  char* param;
+  const char* grad;
+  char* m;
+  char* v;
+  uint8_t* m_scale;
+  uint8_t* v_scale;
+  char* copy;
+  int left;       // elements from there to the tensor's end, at most kTile; negative: no more tiles
+  int flags;      // of the tensor
+  unsigned key;   // of the rounding draws
+  unsigned elem;  // index of the first element, low half
+  float neg_lr, decay;
+  int staged;     // the tile's data are in the ring
+  int pad;
+};
+constexpr int kDescWords = sizeof(TileDesc) / 8;
+static_assert(kDescWords == 11, "written as 8-byte words, one by each lane");
+
+// A tile in shared memory: parameters, gradients, moments and, in 8 bits,
+// scales, one behind the other.
+__host__ __device__ constexpr int type_bytes(int dtype) { return dtype == SHAMPOO_DTYPE_F32 ? 4 : 2; }
+__host__ __device__ constexpr int staged_bytes(bool eight, int pt, int gt) {
+  return kTile * (type_bytes(pt) + type_bytes(gt) + (eight ? 2 : 8)) + (eight ? 2 * kTileBlocks : 0);
+}
+template <bool kEight>
+struct StagedAt {
+  int grad, m, v, m_scale, v_scale;  // offsets; the parameters are at 0
+  __device__ __forceinline__ StagedAt(int pt, int gt)
+      : grad(kTile * type_bytes(pt)), m(grad + kTile * type_bytes(gt)), v(m + kTile * (kEight ? 1 : 4)),
+        m_scale(v + kTile), v_scale(m_scale + kTileBlocks) {}
+};
+
+__device__ __forceinline__ void load8_shared(const unsigned char* base, int i, int dtype, Raw8& r) {
+  if (dtype == SHAMPOO_DTYPE_F32) {
+    const uint4 a = *reinterpret_cast<const uint4*>(base + 32 * i), b = *reinterpret_cast<const uint4*>(base + 32 * i + 16);
+    r.w[0] = a.x, r.w[1] = a.y, r.w[2] = a.z, r.w[3] = a.w, r.w[4] = b.x, r.w[5] = b.y, r.w[6] = b.z, r.w[7] = b.w;
+  } else {
+    const uint4 a = *reinterpret_cast<const uint4*>(base + 16 * i);
+    r.w[0] = a.x, r.w[1] = a.y, r.w[2] = a.z, r.w[3] = a.w;
+  }
+}
+
+// How a block is read: from the ring's stage, from global memory eight
+// elements to an access, or element by element (a short block, or a tensor
+// without the alignment).
+enum Access { kStaged, kVector, kScalar };
+
+// One block of a tile, 'at' elements into it.  stage: the tile in shared
+// memory, most: where its new maxima go, of which the fetching warp makes the
+// scales (kStaged).  Returns whether a value in this lane is not finite.
+// pt, gt: the tensor's types, constants where the caller has branched on them.
+template <bool kEight, Access kAccess>
+__device__ __forceinline__ bool step_block(const TileDesc& t, int pt, int gt, int at, const AdamwArgs& args,
+                                           const Coefs& k, const unsigned char* stage, float2* most) {
+  constexpr bool vec = kAccess != kScalar;
+  const int lane = threadIdx.x & 31;
+  const int ct = (t.flags >> kCopyShift) & 15;
+  const int left = vec ? kQBlock : min(kQBlock, t.left - at);
+  char* param = t.param + at * (pt == SHAMPOO_DTYPE_F32 ? 4 : 2);
+  const char* grad = t.grad + at * (gt == SHAMPOO_DTYPE_F32 ? 4 : 2);
+  char* copy = t.copy ? t.copy + 2 * at : nullptr;
+  char* cm = t.m + at * (kEight ? 1 : 4);
+  char* cv = t.v + at * (kEight ? 1 : 4);
+  uint8_t* ms_at = t.m_scale + (at >> 8);
+  uint8_t* vs_at = t.v_scale + (at >> 8);
+  const float neg_lr = t.neg_lr, decay = t.decay;
+  const unsigned key = t.key, elem = t.elem + at;
+  // this lane's elements: 8 lane + j of the block, or lane + 32 j
+  constexpr int stride = vec ? 1 : 32;
+  const int i0 = vec ? 8 * lane : lane;
+
+  Raw8 rp, rg, rm, rv;
+  f32x2 m[4], v[4], g[4], p[4], r[4];
+  int ms = 0, vs = 0;
+  if (kAccess == kStaged) {
+    const int i = (at >> 3) + lane;
+    const StagedAt<kEight> off(pt, gt);
+    load8_shared(stage + off.grad, i, gt, rg);
+    load8_shared(stage, i, pt, rp);
+    if (kEight) {
+      const uint2 qm = reinterpret_cast<const uint2*>(stage + off.m)[i], qv = reinterpret_cast<const uint2*>(stage + off.v)[i];
+      rm.w[0] = qm.x, rm.w[1] = qm.y, rv.w[0] = qv.x, rv.w[1] = qv.y;
+      ms = stage[off.m_scale + (at >> 8)];
+      vs = stage[off.v_scale + (at >> 8)];
+    } else {
+      load8_shared(stage + off.m, i, SHAMPOO_DTYPE_F32, rm);
+      load8_shared(stage + off.v, i, SHAMPOO_DTYPE_F32, rv);
+    }
+  } else if (kAccess == kVector) {
+    load8(grad, lane, gt, rg);
+    if (kEight) {
+      const uint2 qm = *(reinterpret_cast<const uint2*>(cm) + lane), qv = *(reinterpret_cast<const uint2*>(cv) + lane);
+      rm.w[0] = qm.x, rm.w[1] = qm.y, rv.w[0] = qv.x, rv.w[1] = qv.y;
+      ms = *ms_at;
+      vs = *vs_at;
+    } else {
+      load8(cm, lane, SHAMPOO_DTYPE_F32, rm);
+      load8(cv, lane, SHAMPOO_DTYPE_F32, rv);
+    }
+    load8(param, lane, pt, rp);
+  } else {
+    if (kEight) {
+      ms = *ms_at;
+      vs = *vs_at;
+      rm.w[0] = rm.w[1] = rv.w[0] = rv.w[1] = 0;
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int i = i0 + 32 * j;
+      const bool in = i < left;
+      rg.w[j] = __float_as_uint(in ? load1(grad, i, gt) : 0.0f);
+      rp.w[j] = __float_as_uint(in ? load1(param, i, pt) : 0.0f);
+      if (kEight) {
+        rm.w[j >> 2] |= in ? static_cast<unsigned>(static_cast<uint8_t>(cm[i])) << (8 * (j & 3)) : 0u;
+        rv.w[j >> 2] |= in ? static_cast<unsigned>(static_cast<uint8_t>(cv[i])) << (8 * (j & 3)) : 0u;
+      } else {
+        rm.w[j] = in ? reinterpret_cast<const unsigned*>(cm)[i] : 0u;
+        rv.w[j] = in ? reinterpret_cast<const unsigned*>(cv)[i] : 0u;
+      }
     }
   }
-  if (worst >= 0x7f800000u) atomicOr(&hdr->bad, 1u);
+  {
+    float x[8], y[8];
+    widen8(rg, vec ? gt : SHAMPOO_DTYPE_F32, x);
+    widen8(rp, vec ? pt : SHAMPOO_DTYPE_F32, y);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      g[j] = pack2(x[2 * j], x[2 * j + 1]);
+      p[j] = pack2(y[2 * j], y[2 * j + 1]);
+    }
+  }
+  if (kEight) {
+    const f32x2 mf = both(m8_factor(ms)), vf = both(v8_factor(vs));
+    m8_values4(rm.w[0], mf, m);
+    m8_values4(rm.w[1], mf, m + 2);
+    v8_values4(rv.w[0], vf, r);
+    v8_values4(rv.w[1], vf, r + 2);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) v[j] = mul2(r[j], r[j]);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      m[j] = pack2(__uint_as_float(rm.w[2 * j]), __uint_as_float(rm.w[2 * j + 1]));
+      v[j] = pack2(__uint_as_float(rv.w[2 * j]), __uint_as_float(rv.w[2 * j + 1]));
+    }
+  }
+
+  float mmax = 0.0f, rmax = 0.0f;
+  f32x2 zero = 0ull;  // the sum of 0 p: NaN where a parameter is not finite
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const f32x2 gs2 = mul2(g[j], both(k.coef));
+    m[j] = add2(mul2(m[j], pair(args.beta1)), mul2(gs2, pair(args.om1)));
+    v[j] = add2(mul2(v[j], pair(args.beta2)), mul2(mul2(gs2, pair(args.om2)), gs2));
+    r[j] = kEight ? root2(v[j]) : pack2(root(low(v[j])), root(high(v[j])));
+    const f32x2 den = fma2(r[j], both(k.d1), both(k.d0));
+    const f32x2 ratio = mul2(m[j], pack2(reciprocal(low(den)), reciprocal(high(den))));
+    p[j] = fma2(both(neg_lr), fma2(both(decay), p[j], ratio), p[j]);
+  }
+  if (!vec) {  // nothing behind the tensor's end counts
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if (i0 + 64 * j >= left) m[j] = v[j] = r[j] = p[j] = 0ull;
+      if (i0 + 64 * j + 32 >= left) {
+        m[j] &= 0xffffffffull, v[j] &= 0xffffffffull, r[j] &= 0xffffffffull, p[j] &= 0xffffffffull;
+      }
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    mmax = max_abs3(mmax, low(m[j]), high(m[j]));
+    rmax = kEight ? max_abs3(rmax, low(r[j]), high(r[j])) : max_abs3(rmax, low(v[j]), high(v[j]));
+    zero = fma2(p[j], 0ull, zero);
+  }
+  const bool p_bad = low(zero) + high(zero) != 0.0f;
+  const bool bad = p_bad || not_finite(max_abs3(0.0f, mmax, rmax));
+
+  unsigned h[8];
+  if (kEight || pt == SHAMPOO_DTYPE_BF16) {
+    const unsigned x0 = (elem + i0) * kWeyl + key;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) h[j] = draw_bits(x0 + static_cast<unsigned>(stride * j) * kWeyl);
+  }
+
+  if (kEight) {
+    mmax = warp_max(mmax);
+    rmax = warp_max(rmax);
+    const M8Scale mi(mmax);
+    const V8Scale vi(rmax);
+    const f32x2 mu = both(mi.inverse()), vu = both(vi.inverse());
+    unsigned a[8], b[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const f32x2 x = mul2(mul2(m[j / 2], mu), both(kM8Down)), y = mul2(mul2(r[j / 2], vu), both(kV8Down));
+      const float xm = j & 1 ? high(x) : low(x), xr = j & 1 ? high(y) : low(y);
+      const float mj = j & 1 ? high(m[j / 2]) : low(m[j / 2]);
+      a[j] = m8_code(__float_as_uint(xm), mj, __byte_perm(h[j], 0, 0x4324));
+      b[j] = v8_code(__float_as_uint(xr), __byte_perm(h[j], 0, 0x4104));
+    }
+    const uint2 am = make_uint2(top_bytes(a[0], a[1], a[2], a[3]), top_bytes(a[4], a[5], a[6], a[7]));
+    uint2 bv = make_uint2(top_bytes(b[0], b[1], b[2], b[3]), top_bytes(b[4], b[5], b[6], b[7]));
+    if (zero_bytes(bv.x) | zero_bytes(bv.y)) {
+      bv.x = v8_floor(bv.x, r);
+      bv.y = v8_floor(bv.y, r + 2);
+    }
+    if (kAccess == kStaged) {
+      if (lane == 0) most[at >> 8] = make_float2(mmax, rmax);
+    } else if (lane == 0) {
+      *ms_at = mi.byte(mmax);
+      *vs_at = vi.byte(rmax);
+    }
+    if (vec) {
+      *(reinterpret_cast<uint2*>(cm) + lane) = am;
+      *(reinterpret_cast<uint2*>(cv) + lane) = bv;
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (i0 + 32 * j < left) {
+          cm[i0 + 32 * j] = static_cast<char>((j < 4 ? am.x : am.y) >> (8 * (j & 3)));
+          cv[i0 + 32 * j] = static_cast<char>((j < 4 ? bv.x : bv.y) >> (8 * (j & 3)));
+        }
+    }
+  } else if (vec) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      rm.w[2 * j] = __float_as_uint(low(m[j])), rm.w[2 * j + 1] = __float_as_uint(high(m[j]));
+      rv.w[2 * j] = __float_as_uint(low(v[j])), rv.w[2 * j + 1] = __float_as_uint(high(v[j]));
+    }
+    store32B(reinterpret_cast<float*>(cm) + 8 * lane, rm.w);
+    store32B(reinterpret_cast<float*>(cv) + 8 * lane, rv.w);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (i0 + 32 * j < left) {
+        reinterpret_cast<float*>(cm)[i0 + 32 * j] = j & 1 ? high(m[j / 2]) : low(m[j / 2]);
+        reinterpret_cast<float*>(cv)[i0 + 32 * j] = j & 1 ? high(v[j / 2]) : low(v[j / 2]);
+      }
+  }
+
+  float y[8];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) y[2 * j] = low(p[j]), y[2 * j + 1] = high(p[j]);
+  if (pt == SHAMPOO_DTYPE_F32) {
+    if (vec) {
+      store8(param, lane, SHAMPOO_DTYPE_F32, y);
+      if (copy) store8(copy, lane, ct, y);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (i0 + 32 * j < left) {
+          reinterpret_cast<float*>(param)[i0 + 32 * j] = y[j];
+          if (copy) store1(copy, i0 + 32 * j, ct, y[j]);
+        }
+    }
+  } else {
+    unsigned w[8];
+    if (__any_sync(0xffffffffu, p_bad)) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) w[j] = not_finite(y[j]) ? bf16_not_finite(y[j]) : bf16_up(y[j], h[j]);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) w[j] = bf16_up(y[j], h[j]);
+    }
+    if (vec) {
+      *(reinterpret_cast<uint4*>(param) + lane) =
+          make_uint4(__byte_perm(w[0], w[1], 0x7632), __byte_perm(w[2], w[3], 0x7632),
+                     __byte_perm(w[4], w[5], 0x7632), __byte_perm(w[6], w[7], 0x7632));
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (i0 + 32 * j < left) reinterpret_cast<unsigned short*>(param)[i0 + 32 * j] = static_cast<unsigned short>(w[j] >> 16);
+    }
+  }
+  return bad;
+}
+
+__device__ __forceinline__ Coefs step_coefs(const AdamwArgs& a, const AdamwHeader* hdr) {
+  Coefs k;
+  k.coef = a.coef ? *a.coef : 1.0f;
+  k.lr = a.lr_device ? *a.lr_device : a.lr;
+  k.d1 = a.step ? a.d1 : hdr->d1;
+  k.d0 = a.step ? a.d0 : hdr->d0;
+  return k;
+}
+__device__ __forceinline__ unsigned step_key(const AdamwArgs& a, int t) {
+  return key_word(key_word(key_word(0u, a.seed_lo), a.seed_hi), static_cast<unsigned>(t));
+}
+
+// The last block of the grid writes the status word and, unless the step was
+// skipped, moves the counter on.
+__device__ __forceinline__ void finish_step(const AdamwArgs& a, AdamwHeader* hdr, int t, bool skip) {
   if (!last_block(&hdr->ticket) || threadIdx.x != 0) return;
-  const unsigned bad = atomicExch(&hdr->bad, 0u);
-  hdr->status = (bad || skip) ? kStatusNonFinite : 0u;
+  hdr->status = atomicExch(&hdr->bad, 0u) | (skip ? kStatusNonFinite : 0u);
+  hdr->next = 0;
   if (skip) return;
-  const double p1 = a.step ? a.pow1 : hdr->pow1 * static_cast<double>(a.beta1);
-  const double p2 = a.step ? a.pow2 : hdr->pow2 * static_cast<double>(a.beta2);
+  const double b1 = a.beta1.x, b2 = a.beta2.x;
+  const double p1 = a.step ? a.pow1 : hdr->pow1 * b1, p2 = a.step ? a.pow2 : hdr->pow2 * b2;
+  const double n1 = 1.0 - p1 * b1, n2 = 1.0 - p2 * b2;
   hdr->t = t;
   hdr->pow1 = p1;
   hdr->pow2 = p2;
-  hdr->c1 = static_cast<float>(1.0 / (1.0 - p1 * static_cast<double>(a.beta1)));
-  hdr->c2 = static_cast<float>(sqrt(1.0 / (1.0 - p2 * static_cast<double>(a.beta2))));
+  hdr->d1 = static_cast<float>(n1 / sqrt(n2));
+  hdr->d0 = static_cast<float>(a.eps * n1);
+}
+
+__device__ __forceinline__ int param_type(const TileDesc& t) { return (t.flags >> kParamShift) & 15; }
+__device__ __forceinline__ int grad_type(const TileDesc& t) { return (t.flags >> kGradShift) & 15; }
+__device__ __forceinline__ bool vector_block(const TileDesc& t, int at) {
+  return (t.flags & kFlagVec) && t.left - at >= kQBlock;
+}
+
+// A block of a staged tile, with its types as constants.
+template <bool kEight>
+__device__ __forceinline__ bool step_staged(const TileDesc& t, int at, const AdamwArgs& args, const Coefs& k,
+                                            const unsigned char* stage, float2* most) {
+  constexpr int f32 = SHAMPOO_DTYPE_F32, b16 = SHAMPOO_DTYPE_BF16, f16 = SHAMPOO_DTYPE_F16;
+  const int gt = grad_type(t);
+  if (param_type(t) == f32) {
+    if (gt == f32) return step_block<kEight, kStaged>(t, f32, f32, at, args, k, stage, most);
+    if (gt == b16) return step_block<kEight, kStaged>(t, f32, b16, at, args, k, stage, most);
+    return step_block<kEight, kStaged>(t, f32, f16, at, args, k, stage, most);
+  }
+  if (gt == f32) return step_block<kEight, kStaged>(t, b16, f32, at, args, k, stage, most);
+  if (gt == b16) return step_block<kEight, kStaged>(t, b16, b16, at, args, k, stage, most);
+  return step_block<kEight, kStaged>(t, b16, f16, at, args, k, stage, most);
+}
+
+// Blocks that are not in shared memory, kept out of line.
+template <int kBits>
+__device__ __noinline__ bool step_direct(const TileDesc& t, int at, const AdamwArgs& args, const Coefs& k) {
+  const int pt = param_type(t), gt = grad_type(t);
+  if (kBits == 8 || (kBits == 0 && (t.flags & kFlagEight)))
+    return vector_block(t, at) ? step_block<true, kVector>(t, pt, gt, at, args, k, nullptr, nullptr)
+                               : step_block<true, kScalar>(t, pt, gt, at, args, k, nullptr, nullptr);
+  return vector_block(t, at) ? step_block<false, kVector>(t, pt, gt, at, args, k, nullptr, nullptr)
+                             : step_block<false, kScalar>(t, pt, gt, at, args, k, nullptr, nullptr);
+}
+
+// One block of threads an SM.  One of its warps fetches tiles of 16 blocks
+// with bulk copies into a ring of stages in shared memory, ahead of the 15
+// that compute.  It also forms and writes a finished tile's new scales: a byte
+// for every block, written by its own warp, cost 7 to 10% of the step.  A tile
+// that bulk copies cannot fetch (a tensor's short end, or other alignment) is
+// only described in the ring, and read from global memory by the warps
+// themselves.
+//
+// Long lists are dealt out from a counter, since SMs differ in how far from
+// memory they are: with equal parts 32-bit steps took 10% longer.  See Deal.
+constexpr int kRingWarps = 15;  // and the fetching one: 4 to a scheduler, 128 registers a thread
+constexpr int kRingThreads = (kRingWarps + 1) * 32;
+constexpr int kMaxStages = 4;
+constexpr int kLongList = 16;  // tiles a block
+constexpr int kDeal = 4;       // tiles of one share
+constexpr int kSmemLimit = 226 * 1024;  // of an SM's 227 KB; a little is static
+struct Ring {
+  TileDesc tile[kMaxStages];  // left < 0: no more tiles
+  float2 most[kMaxStages][kTileBlocks];
+  uint64_t full[kMaxStages];   // a tile is there
+  uint64_t empty[kMaxStages];  // every warp is done with it
+  int abort;
+};
+constexpr int kRingHead = (sizeof(Ring) + 127) / 128 * 128;
+
+__device__ __forceinline__ void give_up(Ring& ring, AdamwHeader* hdr) {
+  *const_cast<volatile int*>(&ring.abort) = 1;
+  atomicOr(&hdr->bad, kStatusTimeout);
+}
+
+// The new scales of a staged tile: lanes 0 to 15 have a block's of m, the
+// others of v.  old_scale: where this lane's goes, or null; 'most': the
+// block's maxima.
+__device__ __forceinline__ uint8_t* old_scale(const TileDesc& t) {
+  const int lane = threadIdx.x & 31;
+  uint8_t* to = lane < kTileBlocks ? t.m_scale + lane : t.v_scale + (lane - kTileBlocks);
+  return t.staged && (t.flags & kFlagEight) ? to : nullptr;
+}
+__device__ __forceinline__ void write_scale(uint8_t* to, float2 most) {
+  *to = (threadIdx.x & 31) < kTileBlocks ? M8Scale(most.x).byte(most.x) : V8Scale(most.y).byte(most.y);
+}
+
+// A long list's tiles, dealt to the grid's blocks: share p < 'whole' is kDeal
+// tiles, a grid's width apart, so that blocks that run side by side read side
+// by side (kDeal tiles in a row, all blocks a multiple of that apart, cost
+// 8%); the last one or two grids of shares are single tiles.
+struct Deal {
+  int grid, whole, tile, left;  // tile: the current one; left: tiles behind it in its share
+  __device__ __forceinline__ Deal(int n_tiles, int grid) : grid(grid), whole((n_tiles / (kDeal * grid) - 1) * grid) {}
+  __device__ __forceinline__ void take(int p) {
+    const bool single = p >= whole;
+    tile = single ? kDeal * whole + (p - whole) : p / grid * (kDeal * grid) + p % grid;
+    left = single ? 0 : kDeal - 1;
+  }
+};
+
+// One tensor's arrays as the lanes of the fetching warp see them: lanes 0 to 6
+// have one pointer each, in the order of AdamwTensorDev and TileDesc.
+struct Arrays {
+  char* at;            // lane's array
+  unsigned rate;       // its bytes for 256 elements
+  unsigned to, bytes;  // where a tile of it goes in a stage, and its size; 0: not copied
+  long long n;
+  int first_tile, flags;
+  unsigned tensor_key, key;
+  int high;            // of the element's index, for which 'key' is
+  float neg_lr, decay;
+};
+__device__ __forceinline__ Arrays arrays_of(const AdamwTensorDev& t, float lr, unsigned base) {
+  const int lane = threadIdx.x & 31;
+  Arrays a;
+  a.n = t.n;
+  a.first_tile = t.first_tile;
+  a.flags = t.flags;
+  a.tensor_key = key_word(base, static_cast<unsigned>(t.index));
+  a.key = key_word(a.tensor_key, 0u);
+  a.high = 0;
+  a.neg_lr = -(lr * t.lr_scale);
+  a.decay = t.decay;
+  const bool eight = t.flags & kFlagEight;
+  const unsigned p = 256u * type_bytes((t.flags >> kParamShift) & 15), g = 256u * type_bytes((t.flags >> kGradShift) & 15);
+  const unsigned m = eight ? 256u : 1024u;
+  a.at = lane < 7 ? reinterpret_cast<char* const*>(&t)[lane] : nullptr;
+  a.rate = lane == 0 ? p : lane == 1 ? g : lane < 4 ? m : lane < 6 ? 1u : 512u;
+  const unsigned before = (lane > 0 ? p : 0u) + (lane > 1 ? g : 0u) + (lane > 2 ? m : 0u) + (lane > 3 ? m : 0u) + (lane > 4 ? 1u : 0u);
+  a.to = before * (kTile / 256);
+  a.bytes = lane < (eight ? 6 : 4) ? a.rate * (kTile / 256) : 0u;
+  return a;
+}
+
+// One warp: tiles from the list to the ring, and their scales back.  Stage s
+// gets its i-th tile when the warps have emptied it of the one before.  What
+// is issued here is done in few, wide steps: among 15 busy warps an
+// instruction of this one takes a dozen cycles, and a tile has under 3000.
+__device__ __forceinline__ void fetch_tiles(const AdamwTable& table, Ring& ring, unsigned char* stages, int n_stages,
+                                            int stride, float lr, unsigned base, AdamwHeader* hdr) {
+  const int lane = threadIdx.x & 31, grid = gridDim.x;
+  const bool dealt = table.n_tiles / kLongList >= grid;
+  Deal deal(table.n_tiles, grid);
+  deal.take(blockIdx.x);
+  int tile = dealt ? deal.tile : blockIdx.x, next = 0;
+  bool ask = true;  // at the first tile of a share, or of all
+  int at = -1, s = 0;
+  unsigned i = 0;  // the ring's turn
+  bool ok = true, more = true;
+  Arrays a;
+  while (more) {
+    more = tile < table.n_tiles;
+    unsigned long long word = lane == 7 ? 0xffffffffull : 0ull;  // this lane's of the description; left: -1
+    bool staged = false;
+    char* from = nullptr;
+    if (more) {
+      // the next share, looked at when this one is through: asked for and awaited tile by tile it cost 10%
+      if (dealt && ask && lane == 0) next = static_cast<int>(atomicAdd(&hdr->next, 1u));
+      if (at < 0 || tile < a.first_tile || static_cast<long long>(tile - a.first_tile) * kTile >= a.n) {
+        // another tensor; a new share may begin before the end of the last
+        at = ask ? first_tensor(table.first_tile, table.n_tensors, tile)
+                 : find_tensor(table.first_tile, table.n_tensors, tile, at);
+        a = arrays_of(table.tensors[at], lr, base);
+      }
+      ask = false;
+      const long long e0 = static_cast<long long>(tile - a.first_tile) * kTile;
+      const int left = static_cast<int>(min(static_cast<long long>(kTile), a.n - e0)), high = static_cast<int>(e0 >> 32);
+      if (high != a.high) {
+        a.high = high;
+        a.key = key_word(a.tensor_key, static_cast<unsigned>(high));
+      }
+      staged = (a.flags & kFlagBulk) && left == kTile;
+      from = a.at ? a.at + ((static_cast<unsigned long long>(e0) * a.rate) >> 8) : nullptr;
+      const unsigned lo = lane == 7 ? left : lane == 8 ? a.key : lane == 9 ? __float_as_uint(a.neg_lr) : staged;
+      const unsigned hi = lane == 7 ? a.flags : lane == 8 ? static_cast<unsigned>(e0) : lane == 9 ? __float_as_uint(a.decay) : 0u;
+      word = lane < 7 ? reinterpret_cast<unsigned long long>(from) : lo | (static_cast<unsigned long long>(hi) << 32);
+    }
+    uint8_t* scale = nullptr;  // of the stage's old tile
+    float2 most;
+    if (i > 0) {
+      ok = __all_sync(0xffffffffu, mbar_wait_sleep(&ring.empty[s], (i - 1) & 1, &ring.abort));
+      if (!ok) break;
+      scale = old_scale(ring.tile[s]);
+      most = ring.most[s][lane & (kTileBlocks - 1)];
+      __syncwarp();
+    }
+    if (lane < kDescWords) reinterpret_cast<unsigned long long*>(&ring.tile[s])[lane] = word;
+    __syncwarp();
+    uint64_t* bar = &ring.full[s];
+    if (lane == 0) {
+      if (staged) mbar_arrive_expect_tx(bar, staged_bytes(a.flags & kFlagEight, (a.flags >> kParamShift) & 15, (a.flags >> kGradShift) & 15));
+      else mbar_arrive(bar);
+    }
+    __syncwarp();
+    if (staged && a.bytes) bulk_load(stages + s * stride + a.to, from, a.bytes, bar);
+    if (scale) write_scale(scale, most);
+    __syncwarp();
+    if (!dealt || deal.left-- > 0) {
+      tile += grid;
+    } else {
+      deal.take(grid + __shfl_sync(0xffffffffu, next, 0));
+      tile = deal.tile;
+      ask = true;
+    }
+    if (++s == n_stages) s = 0, ++i;
+  }
+  // the stages behind the last tile's, in turn: what is still in them is finished
+  for (int j = 1; ok && j < n_stages; ++j) {
+    if (i > 0) {
+      ok = __all_sync(0xffffffffu, mbar_wait_sleep(&ring.empty[s], (i - 1) & 1, &ring.abort));
+      uint8_t* scale = ok ? old_scale(ring.tile[s]) : nullptr;
+      if (scale) write_scale(scale, ring.most[s][lane & (kTileBlocks - 1)]);
+    }
+    if (++s == n_stages) s = 0, ++i;
+  }
+  if (!ok) {
+    give_up(ring, hdr);
+    // copies in flight land before the block ends: each stage's last tile, of this turn or the one before
+    int never = 0;
+    for (int j = 0; j < n_stages; ++j) {
+      const int turn = static_cast<int>(i) - (j < s ? 0 : 1);
+      if (turn >= 0) mbar_wait(&ring.full[j], turn & 1, &never);
+    }
+  }
+}
+
+// kBits: 32 or 8, where all of the list's moments have them, or 0 for both.
+template <int kBits>
+__device__ __forceinline__ void adamw_step(const AdamwTable& table, AdamwHeader* hdr, const AdamwArgs& a,
+                                           int n_stages, int stride) {
+  extern __shared__ unsigned char raw[];
+  Ring& ring = *reinterpret_cast<Ring*>((reinterpret_cast<uintptr_t>(raw) + 127) & ~static_cast<uintptr_t>(127));
+  unsigned char* stages = reinterpret_cast<unsigned char*>(&ring) + kRingHead;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const Coefs k = step_coefs(a, hdr);
+  const int t = a.step ? a.step : hdr->t + 1;
+  const bool skip = not_finite(k.coef);  // non-finite gradients: the step is not taken
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < n_stages; ++s) {
+      mbar_init(&ring.full[s], 1);
+      mbar_init(&ring.empty[s], kRingWarps);
+    }
+    ring.abort = 0;
+    fence_mbar_init();
+  }
+  __syncthreads();
+  if (!skip && warp == kRingWarps) {
+    fetch_tiles(table, ring, stages, n_stages, stride, k.lr, step_key(a, t), hdr);
+  } else if (!skip) {
+    // the tiles' blocks are dealt to the warps one after another; every warp waits for every tile and arrives when
+    // done with it, also where it has no block, so that a stage's phases cannot run ahead of a warp
+    bool bad = false;
+    unsigned parity = 0;
+    for (int s = 0, i = warp;;) {
+      const bool ok = mbar_wait(&ring.full[s], parity, &ring.abort);
+      if (!__all_sync(0xffffffffu, ok)) {
+        give_up(ring, hdr);
+        break;
+      }
+      const TileDesc& d = ring.tile[s];
+      if (d.left < 0) break;
+      for (; i < kTileBlocks; i += kRingWarps) {
+        const int at = i * kQBlock;
+        const bool eight = kBits == 8 || (kBits == 0 && (d.flags & kFlagEight));
+        if (d.staged) {
+          bad |= eight ? step_staged<true>(d, at, a, k, stages + s * stride, ring.most[s])
+                       : step_staged<false>(d, at, a, k, stages + s * stride, nullptr);
+        } else if (at < d.left) {
+          bad |= step_direct<kBits>(d, at, a, k);
+        }
+      }
+      i -= kTileBlocks;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ring.empty[s]);
+      if (++s == n_stages) s = 0, parity ^= 1;
+    }
+    if (bad) atomicOr(&hdr->bad, kStatusNonFinite);
+  }
+  finish_step(a, hdr, t, skip);
+}
+
+__global__ void __launch_bounds__(kRingThreads, 1) adamw32_kernel(const __grid_constant__ AdamwTable table,
+                                                                  AdamwHeader* hdr,
+                                                                  const __grid_constant__ AdamwArgs a, int n_stages,
+                                                                  int stride) {
+  adamw_step<32>(table, hdr, a, n_stages, stride);
+}
+__global__ void __launch_bounds__(kRingThreads, 1) adamw8_kernel(const __grid_constant__ AdamwTable table,
+                                                                 AdamwHeader* hdr,
+                                                                 const __grid_constant__ AdamwArgs a, int n_stages,
+                                                                 int stride) {
+  adamw_step<8>(table, hdr, a, n_stages, stride);
+}
+__global__ void __launch_bounds__(kRingThreads, 1) adamw_mixed_kernel(const __grid_constant__ AdamwTable table,
+                                                                      AdamwHeader* hdr,
+                                                                      const __grid_constant__ AdamwArgs a,
+                                                                      int n_stages, int stride) {
+  adamw_step<0>(table, hdr, a, n_stages, stride);
 }
 
 // ---------------------------------------------------------------- moments in and out
 
 // From flat fp32 moments into the list's own: 8-bit tensors are rounded to
 // nearest, 32-bit ones copied.
-__global__ void __launch_bounds__(kListThreads) load_moments_kernel(const AdamwChunk* __restrict__ chunks,
-                                                                    int n_chunks, AdamwHeader* hdr,
+__global__ void __launch_bounds__(kListThreads) load_moments_kernel(const AdamwTable table, AdamwHeader* hdr,
                                                                     const float* __restrict__ m_in,
                                                                     const float* __restrict__ v_in) {
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  unsigned worst = 0;
-  for (int n = blockIdx.x; n < n_chunks; n += gridDim.x) {
-    const AdamwChunk c = chunks[n];
-    const float* fm = m_in + c.flat;
-    const float* fv = v_in + c.flat;
-    for (int b = warp * kQBlock; b < c.count; b += kListWarps * kQBlock) {
-      const bool vec = (c.flags & kFlagVec) && b + kQBlock <= c.count;
-      const int i0 = vec ? b + 8 * lane : b + lane, stride = vec ? 1 : 32;
-      float m[8], v[8];
-      if (vec) {
-        Raw8 rm, rv;
-        load32B(fm + i0, rm.w);
-        load32B(fv + i0, rv.w);
+  const int lane = threadIdx.x & 31;
+  int b = blockIdx.x * kListWarps + (threadIdx.x >> 5);
+  if (b >= table.n_blocks) return;
+  int at = first_tensor(table.first, table.n_tensors, b);
+  bool bad = false;
+  for (; b < table.n_blocks; b += gridDim.x * kListWarps) {
+    at = find_tensor(table.first, table.n_tensors, b, at);
+    const AdamwTensorDev& t = table.tensors[at];
+    const long long e0 = static_cast<long long>(b - t.first) * kQBlock;
+    const int left = static_cast<int>(min(static_cast<long long>(kQBlock), t.n - e0));
+    const bool vec = (t.flags & kFlagVec) && left == kQBlock;
+    const int i0 = vec ? 8 * lane : lane;
+    const float* fm = m_in + static_cast<long long>(b) * kQBlock;
+    const float* fv = v_in + static_cast<long long>(b) * kQBlock;
+    float m[8], v[8], r[8];
+    if (vec) {
+      Raw8 rm, rv;
+      load32B(fm + i0, rm.w);
+      load32B(fv + i0, rv.w);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) m[j] = __uint_as_float(rm.w[j]), v[j] = __uint_as_float(rv.w[j]);
-      } else {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const bool in = i0 + 32 * j < c.count;
-          m[j] = in ? fm[i0 + 32 * j] : 0.0f;
-          v[j] = in ? fv[i0 + 32 * j] : 0.0f;
-        }
-      }
-      unsigned mmax = 0, rmax = 0;
-      float r[8];
+      for (int j = 0; j < 8; ++j) m[j] = __uint_as_float(rm.w[j]), v[j] = __uint_as_float(rv.w[j]);
+    } else {
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        r[j] = __fsqrt_rn(v[j]);
-        mmax = max(mmax, magnitude(m[j]));
-        rmax = max(rmax, magnitude(r[j]));
+        const bool in = i0 + 32 * j < left;
+        m[j] = in ? fm[i0 + 32 * j] : 0.0f;
+        v[j] = in ? fv[i0 + 32 * j] : 0.0f;
       }
-      worst = max(worst, max(mmax, rmax));
-      if (!(c.flags & kFlagEight)) {
-        if (vec) {
-          store8(c.m, i0 >> 3, SHAMPOO_DTYPE_F32, m);
-          store8(c.v, i0 >> 3, SHAMPOO_DTYPE_F32, v);
-        } else {
+    }
+    float mmax = 0.0f, rmax = 0.0f;
 #pragma unroll
-          for (int j = 0; j < 8; ++j)
-            if (i0 + 32 * j < c.count) {
-              static_cast<float*>(c.m)[i0 + 32 * j] = m[j];
-              static_cast<float*>(c.v)[i0 + 32 * j] = v[j];
-            }
-        }
-        continue;
-      }
-      const int mi = m8_scale(__reduce_max_sync(0xffffffffu, mmax));
-      const int vi = v8_scale(__reduce_max_sync(0xffffffffu, rmax));
-      const float mu = inverse_scale(mi), vu = inverse_scale(vi);
-      unsigned cm[8], cv[8];
+    for (int j = 0; j < 8; ++j) r[j] = __fsqrt_rn(v[j]);
+#pragma unroll
+    for (int j = 0; j < 8; j += 2) {
+      mmax = max_abs3(mmax, m[j], m[j + 1]);
+      rmax = max_abs3(rmax, r[j], r[j + 1]);
+    }
+    bad |= not_finite(max_abs3(mmax, rmax, 0.0f));
+    if (t.flags & kFlagEight) {
+      uint8_t* cm = static_cast<uint8_t*>(t.m) + e0;
+      uint8_t* cv = static_cast<uint8_t*>(t.v) + e0;
+      mmax = warp_max(mmax);
+      rmax = warp_max(rmax);
+      const M8Scale mi(mmax);
+      const V8Scale vi(rmax);
+      const float mu = mi.inverse(), vu = vi.inverse();
+      unsigned ca[8], cb[8];
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        cm[j] = m8_nearest(m[j], mu);
-        cv[j] = v8_nearest(r[j], vu);
+        const unsigned x = __float_as_uint(__fmul_rn(__fmul_rn(m[j], mu), kM8Down));
+        const unsigned y = __float_as_uint(__fmul_rn(__fmul_rn(r[j], vu), kV8Down));
+        ca[j] = m8_code(x, m[j], nearest_even(x, kM8Shift));
+        cb[j] = v8_code(y, nearest_even(y, kV8Shift));
+      }
+      const uint2 am = make_uint2(top_bytes(ca[0], ca[1], ca[2], ca[3]), top_bytes(ca[4], ca[5], ca[6], ca[7]));
+      uint2 bv = make_uint2(top_bytes(cb[0], cb[1], cb[2], cb[3]), top_bytes(cb[4], cb[5], cb[6], cb[7]));
+      if (zero_bytes(bv.x) | zero_bytes(bv.y)) {
+        const f32x2 r2[4] = {pack2(r[0], r[1]), pack2(r[2], r[3]), pack2(r[4], r[5]), pack2(r[6], r[7])};
+        bv.x = v8_floor(bv.x, r2);
+        bv.y = v8_floor(bv.y, r2 + 2);
       }
       if (lane == 0) {
-        c.m_scale[b >> 8] = static_cast<uint8_t>(mi);
-        c.v_scale[b >> 8] = static_cast<uint8_t>(vi);
+        t.m_scale[e0 >> 8] = mi.byte(mmax);
+        t.v_scale[e0 >> 8] = vi.byte(rmax);
       }
       if (vec) {
-        *reinterpret_cast<uint2*>(static_cast<uint8_t*>(c.m) + i0) = make_uint2(pack4(cm), pack4(cm + 4));
-        *reinterpret_cast<uint2*>(static_cast<uint8_t*>(c.v) + i0) = make_uint2(pack4(cv), pack4(cv + 4));
+        *(reinterpret_cast<uint2*>(cm) + lane) = am;
+        *(reinterpret_cast<uint2*>(cv) + lane) = bv;
       } else {
 #pragma unroll
         for (int j = 0; j < 8; ++j)
-          if (i0 + stride * j < c.count) {
-            static_cast<uint8_t*>(c.m)[i0 + stride * j] = static_cast<uint8_t>(cm[j]);
-            static_cast<uint8_t*>(c.v)[i0 + stride * j] = static_cast<uint8_t>(cv[j]);
+          if (i0 + 32 * j < left) {
+            cm[i0 + 32 * j] = static_cast<uint8_t>((j < 4 ? am.x : am.y) >> (8 * (j & 3)));
+            cv[i0 + 32 * j] = static_cast<uint8_t>((j < 4 ? bv.x : bv.y) >> (8 * (j & 3)));
+          }
+      }
+    } else {
+      float* om = static_cast<float*>(t.m) + e0;
+      float* ov = static_cast<float*>(t.v) + e0;
+      if (vec) {
+        store8(om, lane, SHAMPOO_DTYPE_F32, m);
+        store8(ov, lane, SHAMPOO_DTYPE_F32, v);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          if (i0 + 32 * j < left) {
+            om[i0 + 32 * j] = m[j];
+            ov[i0 + 32 * j] = v[j];
           }
       }
     }
   }
-  if (worst >= 0x7f800000u) atomicOr(&hdr->status, kStatusNonFinite);
+  if (bad) atomicOr(&hdr->status, kStatusNonFinite);
 }
 
 // The list's moments as flat fp32 or bf16 values; what lies behind a tensor's
 // end, up to the next multiple of kQBlock, is written as zeros.
-__global__ void __launch_bounds__(kListThreads) read_moments_kernel(const AdamwChunk* __restrict__ chunks,
-                                                                    int n_chunks, void* m_out, void* v_out,
+__global__ void __launch_bounds__(kListThreads) read_moments_kernel(const AdamwTable table, void* m_out, void* v_out,
                                                                     int dtype) {
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int lane = threadIdx.x & 31;
   const size_t size = dtype == SHAMPOO_DTYPE_F32 ? 4 : 2;
-  for (int n = blockIdx.x; n < n_chunks; n += gridDim.x) {
-    const AdamwChunk c = chunks[n];
-    void* om = static_cast<char*>(m_out) + size * c.flat;
-    void* ov = static_cast<char*>(v_out) + size * c.flat;
-    for (int b = warp * kQBlock; b < c.count; b += kListWarps * kQBlock) {
-      const int i0 = b + 8 * lane;
-      const bool vec = (c.flags & kFlagVec) && b + kQBlock <= c.count;
-      float m[8], v[8];
-      if (c.flags & kFlagEight) {
-        unsigned cm[2] = {0, 0}, cv[2] = {0, 0};
-        if (vec) {
-          const uint2 qm = *reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(c.m) + i0);
-          const uint2 qv = *reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(c.v) + i0);
-          cm[0] = qm.x, cm[1] = qm.y, cv[0] = qv.x, cv[1] = qv.y;
-        } else {
+  int b = blockIdx.x * kListWarps + (threadIdx.x >> 5);
+  if (b >= table.n_blocks) return;
+  int at = first_tensor(table.first, table.n_tensors, b);
+  for (; b < table.n_blocks; b += gridDim.x * kListWarps) {
+    at = find_tensor(table.first, table.n_tensors, b, at);
+    const AdamwTensorDev& t = table.tensors[at];
+    const long long e0 = static_cast<long long>(b - t.first) * kQBlock;
+    const int left = static_cast<int>(min(static_cast<long long>(kQBlock), t.n - e0));
+    const bool vec = (t.flags & kFlagVec) && left == kQBlock;
+    const int i0 = 8 * lane;
+    char* om = static_cast<char*>(m_out) + size * kQBlock * b;
+    char* ov = static_cast<char*>(v_out) + size * kQBlock * b;
+    f32x2 m[4], v[4];
+    if (t.flags & kFlagEight) {
+      const uint8_t* cm = static_cast<const uint8_t*>(t.m) + e0;
+      const uint8_t* cv = static_cast<const uint8_t*>(t.v) + e0;
+      uint2 qm = make_uint2(0, 0), qv = make_uint2(0, 0);
+      if (vec) {
+        qm = *(reinterpret_cast<const uint2*>(cm) + lane);
+        qv = *(reinterpret_cast<const uint2*>(cv) + lane);
+      } else {
+        unsigned am[2] = {0, 0}, av[2] = {0, 0};
 #pragma unroll
-          for (int j = 0; j < 8; ++j)
-            if (i0 + j < c.count) {
-              cm[j >> 2] |= static_cast<unsigned>(static_cast<const uint8_t*>(c.m)[i0 + j]) << (8 * (j & 3));
-              cv[j >> 2] |= static_cast<unsigned>(static_cast<const uint8_t*>(c.v)[i0 + j]) << (8 * (j & 3));
-            }
-        }
-        const float mf = m8_factor(c.m_scale[b >> 8]), vf = v8_factor(c.v_scale[b >> 8]);
-        m8_values4(cm[0], mf, m);
-        m8_values4(cm[1], mf, m + 4);
-        v8_values4(cv[0], vf, v);
-        v8_values4(cv[1], vf, v + 4);
+        for (int j = 0; j < 8; ++j)
+          if (i0 + j < left) {
+            am[j >> 2] |= static_cast<unsigned>(cm[i0 + j]) << (8 * (j & 3));
+            av[j >> 2] |= static_cast<unsigned>(cv[i0 + j]) << (8 * (j & 3));
+          }
+        qm = make_uint2(am[0], am[1]);
+        qv = make_uint2(av[0], av[1]);
+      }
+      const f32x2 mf = both(m8_factor(t.m_scale[e0 >> 8])), vf = both(v8_factor(t.v_scale[e0 >> 8]));
+      m8_values4(qm.x, mf, m);
+      m8_values4(qm.y, mf, m + 2);
+      v8_values4(qv.x, vf, v);
+      v8_values4(qv.y, vf, v + 2);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = __fmul_rn(v[j], v[j]);
-      } else if (vec) {
-        Raw8 rm, rv;
-        load32B(static_cast<const float*>(c.m) + i0, rm.w);
-        load32B(static_cast<const float*>(c.v) + i0, rv.w);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) m[j] = __uint_as_float(rm.w[j]), v[j] = __uint_as_float(rv.w[j]);
+      for (int j = 0; j < 4; ++j) v[j] = mul2(v[j], v[j]);
+    } else {
+      const float* fm = static_cast<const float*>(t.m) + e0;
+      const float* fv = static_cast<const float*>(t.v) + e0;
+      Raw8 rm, rv;
+      if (vec) {
+        load32B(fm + i0, rm.w);
+        load32B(fv + i0, rv.w);
       } else {
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-          m[j] = i0 + j < c.count ? static_cast<const float*>(c.m)[i0 + j] : 0.0f;
-          v[j] = i0 + j < c.count ? static_cast<const float*>(c.v)[i0 + j] : 0.0f;
+          rm.w[j] = i0 + j < left ? __float_as_uint(fm[i0 + j]) : 0u;
+          rv.w[j] = i0 + j < left ? __float_as_uint(fv[i0 + j]) : 0u;
         }
       }
-      if (!vec) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-          if (i0 + j >= c.count) m[j] = v[j] = 0.0f;
+      for (int j = 0; j < 4; ++j) {
+        m[j] = pack2(__uint_as_float(rm.w[2 * j]), __uint_as_float(rm.w[2 * j + 1]));
+        v[j] = pack2(__uint_as_float(rv.w[2 * j]), __uint_as_float(rv.w[2 * j + 1]));
       }
-      store8(om, i0 >> 3, dtype, m);
-      store8(ov, i0 >> 3, dtype, v);
     }
+    float x[8], y[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const bool in = vec || i0 + j < left;
+      x[j] = !in ? 0.0f : j & 1 ? high(m[j / 2]) : low(m[j / 2]);
+      y[j] = !in ? 0.0f : j & 1 ? high(v[j / 2]) : low(v[j / 2]);
+    }
+    store8(om, lane, dtype, x);
+    store8(ov, lane, dtype, y);
   }
 }
 
 }  // namespace
 
-int adamw_blocks(int which) {
-  switch (which) {
-    case 0: return resident_blocks(adamw_step_kernel<0>);
-    case 1: return resident_blocks(adamw_step_kernel<1>);
-    case 2: return resident_blocks(adamw_step_kernel<2>);
-    case 3: return resident_blocks(load_moments_kernel);
-    default: return resident_blocks(read_moments_kernel);
-  }
+int adamw_stage_bytes(bool eight, int param_dtype, int grad_dtype) {
+  return (staged_bytes(eight, param_dtype, grad_dtype) + 127) / 128 * 128;
 }
 
-void launch_adamw(const AdamwChunk* chunks, int n, int which, int grid, AdamwHeader* hdr, const AdamwArgs& a,
+template <typename Kernel>
+int prepare(Kernel kernel, std::atomic<unsigned long long>& done, AdamwLaunch* out) {
+  if (smem_limit_once(kernel, kSmemLimit, done) != cudaSuccess) return SHAMPOO_ECUDA;
+  out->step = resident_blocks(kernel, kRingThreads, out->smem);
+  return SHAMPOO_OK;
+}
+
+int adamw_prepare(int bits, int stage_bytes, AdamwLaunch* out) {
+  constexpr int kHead = kRingHead + 128;  // the kernel aligns to 128
+  out->bits = bits;
+  out->stages = std::min(kMaxStages, (kSmemLimit - kHead) / stage_bytes);
+  out->stride = stage_bytes;
+  out->smem = kHead + out->stages * stage_bytes;
+  static std::atomic<unsigned long long> done[3];
+  const int rc = bits == 32  ? prepare(adamw32_kernel, done[0], out)
+                 : bits == 8 ? prepare(adamw8_kernel, done[1], out)
+                             : prepare(adamw_mixed_kernel, done[2], out);
+  if (rc) return rc;
+  out->load = resident_blocks(load_moments_kernel);
+  out->read = resident_blocks(read_moments_kernel);
+  return out->step < 0 || out->load < 0 || out->read < 0 ? SHAMPOO_ECUDA : SHAMPOO_OK;
+}
+
+void launch_adamw(const AdamwTable& t, const AdamwLaunch& l, int grid, AdamwHeader* hdr, const AdamwArgs& a,
                   cudaStream_t st) {
-  if (which == 0) adamw_step_kernel<0><<<grid, kListThreads, 0, st>>>(chunks, n, hdr, a);
-  else if (which == 1) adamw_step_kernel<1><<<grid, kListThreads, 0, st>>>(chunks, n, hdr, a);
-  else adamw_step_kernel<2><<<grid, kListThreads, 0, st>>>(chunks, n, hdr, a);
+  if (l.bits == 32) adamw32_kernel<<<grid, kRingThreads, l.smem, st>>>(t, hdr, a, l.stages, l.stride);
+  else if (l.bits == 8) adamw8_kernel<<<grid, kRingThreads, l.smem, st>>>(t, hdr, a, l.stages, l.stride);
+  else adamw_mixed_kernel<<<grid, kRingThreads, l.smem, st>>>(t, hdr, a, l.stages, l.stride);
   prof_count_launch();
 }
 
-void launch_load_moments(const AdamwChunk* chunks, int n, int grid, AdamwHeader* hdr, const float* m, const float* v,
+void launch_load_moments(const AdamwTable& t, int grid, AdamwHeader* hdr, const float* m, const float* v,
                          cudaStream_t st) {
-  load_moments_kernel<<<grid, kListThreads, 0, st>>>(chunks, n, hdr, m, v);
+  load_moments_kernel<<<grid, kListThreads, 0, st>>>(t, hdr, m, v);
   prof_count_launch();
 }
 
-void launch_read_moments(const AdamwChunk* chunks, int n, int grid, void* m, void* v, int dtype, cudaStream_t st) {
-  read_moments_kernel<<<grid, kListThreads, 0, st>>>(chunks, n, m, v, dtype);
+void launch_read_moments(const AdamwTable& t, int grid, void* m, void* v, int dtype, cudaStream_t st) {
+  read_moments_kernel<<<grid, kListThreads, 0, st>>>(t, m, v, dtype);
   prof_count_launch();
 }
 

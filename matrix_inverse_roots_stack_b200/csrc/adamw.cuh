@@ -1,61 +1,91 @@
-// AdamW over a list of tensors: chunk records and launchers (adamw.cu).
+// AdamW over a list of tensors: table records and launchers (adamw.cu).
 #pragma once
 
 #include "tensor_list.cuh"
 
 namespace dash {
 
-// One chunk of one tensor, all pointers at its first element.  Chunks start
-// at multiples of kQBlock elements, so no block of 8-bit moments is split.
-struct AdamwChunk {
+// One tensor of the list (tensors without elements are left out).  Its blocks
+// of kQBlock elements, the last one short or not, follow those of the tensor
+// before it in one count over the list.
+struct AdamwTensorDev {
   void* param;
   const void* grad;
-  void* copy;        // fp32 parameters may have a 16-bit copy written beside them, or null
   void* m;           // fp32 moments, or 8-bit codes
   void* v;
   uint8_t* m_scale;  // 8-bit: one scale for each block
   uint8_t* v_scale;
-  long long elem;    // first element's index in its tensor
-  long long flat;    // and in the flat moments of the read and load calls
-  int count;         // elements
+  void* copy;        // fp32 parameters may have a 16-bit copy written beside them, or null
+  long long n;
+  int first;         // first block; kQBlock times it is the tensor's place in the flat moments
+  int first_tile;    // first tile of kTile elements, counted over the list in the same way
   int flags;
-  int tensor;        // index in the list
+  int index;         // in the caller's list
   float lr_scale, decay;
-  int pad;
+  int pad[2];
 };
-static_assert(sizeof(AdamwChunk) == 96, "six 16-byte words");
+static_assert(sizeof(AdamwTensorDev) == 96, "six 16-byte words");
 
-constexpr int kParamShift = 0, kGradShift = 4, kCopyShift = 8;  // element types in AdamwChunk::flags
+constexpr int kParamShift = 0, kGradShift = 4, kCopyShift = 8;  // element types in AdamwTensorDev::flags
 constexpr int kFlagEight = 1 << 12;                             // 8-bit moments
 constexpr int kFlagVec = 1 << 13;                               // every pointer allows eight-element accesses
+constexpr int kFlagBulk = 1 << 14;                              // and bulk copies: 16-byte aligned
+
+// Elements that the step takes at a time: 16 blocks, so that their scales are
+// one 16-byte copy.
+constexpr int kTileBlocks = 16;
+constexpr int kTile = kTileBlocks * kQBlock;
+
+// The list on the device: 'first' and 'first_tile' of each tensor; the
+// records.
+struct AdamwTable {
+  const int* first;
+  const int* first_tile;
+  const AdamwTensorDev* tensors;
+  int n_tensors, n_blocks, n_tiles;
+};
 
 // Start of the workspace: the status word, the blocks' arrival count, and the
 // step counter with what the next step's bias corrections need.
 struct AdamwHeader {
   unsigned status;
   unsigned ticket;
-  unsigned bad;          // a non-finite value was met in the running step
+  unsigned bad;          // status bits of the running step
+  unsigned next;         // tiles taken in the running step, beyond the first of each block
   int t;                 // last step taken
   double pow1, pow2;     // beta1^t, beta2^t
-  float c1, c2;          // for step t + 1: 1 / (1 - beta1^(t+1)), sqrt(1 / (1 - beta2^(t+1)))
+  float d1, d0;          // for step t + 1, see AdamwArgs
 };
 
 struct AdamwArgs {
-  float beta1, beta2, eps;
+  // beta, and 1 - beta, as pairs of one value: operands of the packed products, read from the constant bank
+  float2 beta1, om1, beta2, om2;
+  float eps;
   unsigned seed_lo, seed_hi;
   int step;              // > 0: take this step number and the values below; 0: the header's next
-  float c1, c2;
+  // m_hat / (sqrt(v_hat) + eps) = m / (d1 sqrt(v) + d0): d1 = (1 - beta1^t) / sqrt(1 - beta2^t),
+  // d0 = eps (1 - beta1^t)
+  float d1, d0;
   double pow1, pow2;
   float lr;
   const float* lr_device;  // null: lr
   const float* coef;       // null: 1
 };
 
-int adamw_blocks(int which);  // resident blocks of the 0: 32-bit, 1: 8-bit, 2: mixed step, 3: load, 4: read kernel
-void launch_adamw(const AdamwChunk* chunks, int n, int which, int grid, AdamwHeader* hdr, const AdamwArgs& a,
+// How the kernels are launched on the current device: blocks that fill it
+// (step, load, read), and the step's shared memory.
+struct AdamwLaunch {
+  int step, load, read;
+  int bits;                  // 32, 8, or 0 for both
+  int stages, stride, smem;
+};
+int adamw_stage_bytes(bool eight, int param_dtype, int grad_dtype);
+// stage_bytes: the largest adamw_stage_bytes of the list.  Returns a SHAMPOO_* code.
+int adamw_prepare(int bits, int stage_bytes, AdamwLaunch* out);
+void launch_adamw(const AdamwTable& t, const AdamwLaunch& l, int grid, AdamwHeader* hdr, const AdamwArgs& a,
                   cudaStream_t st);
-void launch_load_moments(const AdamwChunk* chunks, int n, int grid, AdamwHeader* hdr, const float* m, const float* v,
+void launch_load_moments(const AdamwTable& t, int grid, AdamwHeader* hdr, const float* m, const float* v,
                          cudaStream_t st);
-void launch_read_moments(const AdamwChunk* chunks, int n, int grid, void* m, void* v, int dtype, cudaStream_t st);
+void launch_read_moments(const AdamwTable& t, int grid, void* m, void* v, int dtype, cudaStream_t st);
 
 }  // namespace dash

@@ -1,38 +1,35 @@
 // Entry points of AdamW over a list of tensors (declared in
-// include/dash_b200.h): argument checks, the chunk table, and the launches of
+// include/dash_b200.h): argument checks, the table, and the launches of
 // adamw.cu's kernels.
-#include <cfloat>
 #include <cmath>
 #include <new>
 
 #include "adamw.cuh"
 #include "profile.cuh"
 
-using dash::AdamwChunk;
 using dash::AdamwHeader;
+using dash::AdamwTable;
+using dash::AdamwTensorDev;
 
 struct shampoo_adamw {
   shampoo_adamw_hparams hp{};
-  std::vector<AdamwChunk> chunks;
+  std::vector<int> first, first_tile;    // of each tensor
+  std::vector<AdamwTensorDev> tensors;
   AdamwHeader start{};         // header that bind uploads
-  int which = 0;               // 0: 32-bit moments only, 1: 8-bit only, 2: both
-  int64_t moment_elems = 0;    // of the flat moments
-  size_t total = 0;            // workspace bytes
+  int bits = 32;               // of every tensor's moments, or 0
+  int stage_bytes = 0;         // of a tile in shared memory, at most
+  int64_t blocks = 0, tiles = 0;
+  size_t off_tiles = 0, off_tensors = 0, total = 0;  // workspace
   const void* bound_ws = nullptr;
-  int step_blocks = 0, load_blocks = 0, read_blocks = 0;
+  dash::AdamwLaunch launch{};
 };
 
 namespace {
 
 constexpr size_t kHeaderBytes = 256;
+constexpr float kMinEps = 1e-30f;  // keeps eps (1 - beta1^t) in fp32's normal range for every beta1 < 1
+constexpr int64_t kMaxBlocks = 0x7fffffff - 0xffff;  // a block's number plus a grid's warps stays an int
 static_assert(sizeof(AdamwHeader) <= kHeaderBytes, "header fits");
-
-// Elements of a chunk: one step of a block's warps, or four where that still
-// leaves the device many chunks for each block.
-int chunk_elems(int64_t total) {
-  const int one = dash::kListWarps * dash::kQBlock;
-  return total > (1ll << 28) ? 4 * one : one;
-}
 
 bool tensor_ok(const shampoo_adamw_tensor& q) {
   if (q.n < 0 || q.n > SHAMPOO_MAX_TENSOR || (q.state_bits != 32 && q.state_bits != 8)) return false;
@@ -59,39 +56,53 @@ bool vector_ok(const shampoo_adamw_tensor& q) {
          dash::aligned_to(q.m, ms) && dash::aligned_to(q.v, ms);
 }
 
-void add_tensor(shampoo_adamw* c, const shampoo_adamw_tensor& q, int index, int chunk) {
-  const size_t ps = dash::dtype_bytes(q.param_dtype), gs = dash::dtype_bytes(q.grad_dtype);
-  const bool eight = q.state_bits == 8;
-  const size_t ms = eight ? 1 : 4;
-  int flags = (q.param_dtype << dash::kParamShift) | (q.grad_dtype << dash::kGradShift) |
-              ((q.copy ? q.copy_dtype : 0) << dash::kCopyShift);
-  if (eight) flags |= dash::kFlagEight;
-  if (vector_ok(q)) flags |= dash::kFlagVec;
-  for (int64_t at = 0; at < q.n; at += chunk) {
-    AdamwChunk r{};
-    r.param = static_cast<char*>(q.param) + ps * at;
-    r.grad = static_cast<const char*>(q.grad) + gs * at;
-    r.copy = q.copy ? static_cast<char*>(q.copy) + 2 * at : nullptr;
-    r.m = static_cast<char*>(q.m) + ms * at;
-    r.v = static_cast<char*>(q.v) + ms * at;
-    r.m_scale = eight ? q.m_scale + at / dash::kQBlock : nullptr;
-    r.v_scale = eight ? q.v_scale + at / dash::kQBlock : nullptr;
-    r.elem = at;
-    r.flat = c->moment_elems + at;
-    r.count = static_cast<int>(std::min<int64_t>(chunk, q.n - at));
-    r.flags = flags;
-    r.tensor = index;
-    r.lr_scale = q.lr_scale;
-    r.decay = q.weight_decay;
-    c->chunks.push_back(r);
-  }
-  c->moment_elems += (q.n + dash::kQBlock - 1) / dash::kQBlock * dash::kQBlock;
+// Whether bulk copies (16-byte aligned) may read it too.
+bool bulk_ok(const shampoo_adamw_tensor& q) {
+  return vector_ok(q) && dash::aligned_to(q.m, 16) && dash::aligned_to(q.v, 16) &&
+         (q.state_bits == 32 || (dash::aligned_to(q.m_scale, 16) && dash::aligned_to(q.v_scale, 16)));
 }
 
-// beta^t and the corrections of step t, in double, from the fp32 betas.
-double pow_beta(float beta, int t) { return std::pow(static_cast<double>(beta), t); }
-float correction1(double p1) { return static_cast<float>(1.0 / (1.0 - p1)); }
-float correction2(double p2) { return static_cast<float>(std::sqrt(1.0 / (1.0 - p2))); }
+void add_tensor(shampoo_adamw* c, const shampoo_adamw_tensor& q, int index) {
+  const bool eight = q.state_bits == 8;
+  AdamwTensorDev r{};
+  r.param = q.param;
+  r.grad = q.grad;
+  r.copy = q.copy;
+  r.m = q.m;
+  r.v = q.v;
+  r.m_scale = eight ? q.m_scale : nullptr;
+  r.v_scale = eight ? q.v_scale : nullptr;
+  r.n = q.n;
+  r.first = static_cast<int>(c->blocks);
+  r.first_tile = static_cast<int>(c->tiles);
+  r.flags = (q.param_dtype << dash::kParamShift) | (q.grad_dtype << dash::kGradShift) |
+            ((q.copy ? q.copy_dtype : 0) << dash::kCopyShift) | (eight ? dash::kFlagEight : 0) |
+            (vector_ok(q) ? dash::kFlagVec : 0) | (bulk_ok(q) ? dash::kFlagBulk : 0);
+  r.index = index;
+  r.lr_scale = q.lr_scale;
+  r.decay = q.weight_decay;
+  c->bits = c->tensors.empty() || c->bits == q.state_bits ? q.state_bits : 0;
+  c->first.push_back(r.first);
+  c->first_tile.push_back(r.first_tile);
+  c->tensors.push_back(r);
+  c->blocks += (q.n + dash::kQBlock - 1) / dash::kQBlock;
+  c->tiles += (q.n + dash::kTile - 1) / dash::kTile;
+  c->stage_bytes = std::max(c->stage_bytes, dash::adamw_stage_bytes(eight, q.param_dtype, q.grad_dtype));
+}
+
+// Step t's constants, in double from the fp32 hyper-parameters.
+struct StepConstants {
+  double pow1, pow2;  // beta^t
+  float d1, d0;
+};
+StepConstants step_constants(const shampoo_adamw_hparams& hp, double t) {
+  StepConstants s;
+  s.pow1 = std::pow(static_cast<double>(hp.beta1), t);
+  s.pow2 = std::pow(static_cast<double>(hp.beta2), t);
+  s.d1 = static_cast<float>((1.0 - s.pow1) / std::sqrt(1.0 - s.pow2));
+  s.d0 = static_cast<float>(hp.adam_eps * (1.0 - s.pow1));
+  return s;
+}
 
 int check_bound(const shampoo_adamw* c, const void* ws, size_t ws_bytes) {
   if (!c) return SHAMPOO_EINVAL;
@@ -99,9 +110,18 @@ int check_bound(const shampoo_adamw* c, const void* ws, size_t ws_bytes) {
   return ws == c->bound_ws ? SHAMPOO_OK : SHAMPOO_EINVAL;
 }
 
-const AdamwChunk* table(const void* ws) {
-  return reinterpret_cast<const AdamwChunk*>(static_cast<const char*>(ws) + kHeaderBytes);
+AdamwTable table(const shampoo_adamw* c, const void* ws) {
+  const char* w = static_cast<const char*>(ws);
+  return {reinterpret_cast<const int*>(w + kHeaderBytes), reinterpret_cast<const int*>(w + c->off_tiles),
+          reinterpret_cast<const AdamwTensorDev*>(w + c->off_tensors), static_cast<int>(c->tensors.size()),
+          static_cast<int>(c->blocks), static_cast<int>(c->tiles)};
 }
+
+// Blocks of threads for so many pieces of work.
+int grid_for(int64_t pieces, int resident) {
+  return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(pieces, resident)));
+}
+int64_t warp_blocks(const shampoo_adamw* c) { return (c->blocks + dash::kListWarps - 1) / dash::kListWarps; }
 
 }  // namespace
 
@@ -112,23 +132,22 @@ int shampoo_adamw_init(shampoo_adamw** out, const shampoo_adamw_tensor* tensors,
   if (!out || !tensors || n_tensors < 1 || !hp || !workspace_bytes) return SHAMPOO_EINVAL;
   *out = nullptr;
   if (!(hp->beta1 >= 0.0f && hp->beta1 < 1.0f) || !(hp->beta2 >= 0.0f && hp->beta2 < 1.0f) ||
-      !(hp->adam_eps >= FLT_MIN) || !std::isfinite(hp->adam_eps))
+      !(hp->adam_eps >= kMinEps) || !std::isfinite(hp->adam_eps))
     return SHAMPOO_EINVAL;
   shampoo_adamw* c = nullptr;
   try {
     c = new shampoo_adamw();
     c->hp = *hp;
     std::vector<dash::ByteRange> ranges;
-    int64_t total = 0;
-    bool has32 = false, has8 = false, ok = true;
+    int64_t blocks_total = 0;
+    bool ok = true;
     for (int i = 0; i < n_tensors && ok; ++i) {
       const shampoo_adamw_tensor& q = tensors[i];
       ok = tensor_ok(q);
       if (!ok || q.n == 0) continue;
       const size_t n = static_cast<size_t>(q.n), ms = q.state_bits == 32 ? 4 : 1;
       const size_t blocks = (n + dash::kQBlock - 1) / dash::kQBlock;
-      (q.state_bits == 32 ? has32 : has8) = true;
-      total += q.n;
+      blocks_total += static_cast<int64_t>(blocks);
       dash::add_range(ranges, q.param, n * dash::dtype_bytes(q.param_dtype), true);
       dash::add_range(ranges, q.grad, n * dash::dtype_bytes(q.grad_dtype), false);
       if (q.copy) dash::add_range(ranges, q.copy, 2 * n, true);
@@ -139,20 +158,22 @@ int shampoo_adamw_init(shampoo_adamw** out, const shampoo_adamw_tensor* tensors,
         dash::add_range(ranges, q.v_scale, blocks, true);
       }
     }
-    const int chunk = chunk_elems(total);
-    if (!ok || dash::ranges_clash(ranges) || total / chunk + n_tensors > 0x7ffffff) {
+    if (!ok || blocks_total > kMaxBlocks || dash::ranges_clash(ranges)) {
       delete c;
       return SHAMPOO_EINVAL;
     }
-    for (int i = 0; i < n_tensors; ++i) add_tensor(c, tensors[i], i, chunk);
-    c->which = has32 && has8 ? 2 : has8 ? 1 : 0;
+    for (int i = 0; i < n_tensors; ++i)
+      if (tensors[i].n > 0) add_tensor(c, tensors[i], i);
+    if (c->tensors.empty()) c->stage_bytes = dash::adamw_stage_bytes(false, SHAMPOO_DTYPE_F32, SHAMPOO_DTYPE_F32);
   } catch (...) {
     delete c;
     return SHAMPOO_EINVAL;
   }
-  c->total = kHeaderBytes + c->chunks.size() * sizeof(AdamwChunk);
+  c->off_tiles = kHeaderBytes + c->first.size() * sizeof(int);
+  c->off_tensors = (c->off_tiles + c->first_tile.size() * sizeof(int) + 255) / 256 * 256;
+  c->total = c->off_tensors + c->tensors.size() * sizeof(AdamwTensorDev);
   *workspace_bytes = c->total;
-  if (moment_elems) *moment_elems = c->moment_elems;
+  if (moment_elems) *moment_elems = c->blocks * dash::kQBlock;
   *out = c;
   return SHAMPOO_OK;
 }
@@ -165,22 +186,26 @@ int shampoo_adamw_bind(shampoo_adamw* c, int steps_taken, void* ws, size_t ws_by
   if (cudaStreamIsCapturing(st, &cap) != cudaSuccess) return SHAMPOO_ECUDA;
   if (cap != cudaStreamCaptureStatusNone) return SHAMPOO_EINVAL;
   c->bound_ws = nullptr;
-  c->step_blocks = dash::adamw_blocks(c->which);
-  c->load_blocks = dash::adamw_blocks(3);
-  c->read_blocks = dash::adamw_blocks(4);
-  if (c->step_blocks < 0 || c->load_blocks < 0 || c->read_blocks < 0) return SHAMPOO_ECUDA;
-  const double p1 = pow_beta(c->hp.beta1, steps_taken), p2 = pow_beta(c->hp.beta2, steps_taken);
+  const int rc = dash::adamw_prepare(c->bits, c->stage_bytes, &c->launch);
+  if (rc) return rc;
+  const StepConstants next = step_constants(c->hp, steps_taken + 1.0);
+  const StepConstants last = step_constants(c->hp, steps_taken);
   c->start = AdamwHeader{};
   c->start.t = steps_taken;
-  c->start.pow1 = p1;
-  c->start.pow2 = p2;
-  c->start.c1 = correction1(p1 * c->hp.beta1);
-  c->start.c2 = correction2(p2 * c->hp.beta2);
-  if (cudaMemcpyAsync(ws, &c->start, sizeof(c->start), cudaMemcpyHostToDevice, st) != cudaSuccess)
+  c->start.pow1 = last.pow1;
+  c->start.pow2 = last.pow2;
+  c->start.d1 = next.d1;
+  c->start.d0 = next.d0;
+  char* w = static_cast<char*>(ws);
+  if (cudaMemcpyAsync(w, &c->start, sizeof(c->start), cudaMemcpyHostToDevice, st) != cudaSuccess)
     return SHAMPOO_ECUDA;
-  if (!c->chunks.empty() &&
-      cudaMemcpyAsync(static_cast<char*>(ws) + kHeaderBytes, c->chunks.data(),
-                      c->chunks.size() * sizeof(AdamwChunk), cudaMemcpyHostToDevice, st) != cudaSuccess)
+  if (!c->tensors.empty() &&
+      (cudaMemcpyAsync(w + kHeaderBytes, c->first.data(), c->first.size() * sizeof(int), cudaMemcpyHostToDevice,
+                       st) != cudaSuccess ||
+       cudaMemcpyAsync(w + c->off_tiles, c->first_tile.data(), c->first_tile.size() * sizeof(int),
+                       cudaMemcpyHostToDevice, st) != cudaSuccess ||
+       cudaMemcpyAsync(w + c->off_tensors, c->tensors.data(), c->tensors.size() * sizeof(AdamwTensorDev),
+                       cudaMemcpyHostToDevice, st) != cudaSuccess))
     return SHAMPOO_ECUDA;
   c->bound_ws = ws;
   return SHAMPOO_OK;
@@ -193,25 +218,26 @@ int shampoo_adamw_step(shampoo_adamw* c, int step, float lr, const float* lr_dev
   if (step < 0 || (!lr_device && !std::isfinite(lr))) return SHAMPOO_EINVAL;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   dash::AdamwArgs a{};
-  a.beta1 = c->hp.beta1;
-  a.beta2 = c->hp.beta2;
+  a.beta1 = make_float2(c->hp.beta1, c->hp.beta1);
+  a.beta2 = make_float2(c->hp.beta2, c->hp.beta2);
+  a.om1 = make_float2(1.0f - c->hp.beta1, 1.0f - c->hp.beta1);
+  a.om2 = make_float2(1.0f - c->hp.beta2, 1.0f - c->hp.beta2);
   a.eps = c->hp.adam_eps;
   a.seed_lo = static_cast<unsigned>(c->hp.seed);
   a.seed_hi = static_cast<unsigned>(c->hp.seed >> 32);
   a.step = step;
   if (step > 0) {
-    a.pow1 = pow_beta(a.beta1, step);
-    a.pow2 = pow_beta(a.beta2, step);
-    a.c1 = correction1(a.pow1);
-    a.c2 = correction2(a.pow2);
+    const StepConstants s = step_constants(c->hp, step);
+    a.pow1 = s.pow1;
+    a.pow2 = s.pow2;
+    a.d1 = s.d1;
+    a.d0 = s.d0;
   }
   a.lr = lr;
   a.lr_device = lr_device;
   a.coef = coef;
-  const int n = static_cast<int>(c->chunks.size());
   const int slot = dash::prof_begin(dash::kProfAdam, st);
-  dash::launch_adamw(table(ws), n, c->which, std::max(1, std::min(n, c->step_blocks)),
-                     static_cast<AdamwHeader*>(ws), a, st);
+  dash::launch_adamw(table(c, ws), c->launch, grid_for(c->tiles, c->launch.step), static_cast<AdamwHeader*>(ws), a, st);
   const cudaError_t e = cudaGetLastError();
   dash::prof_end(slot, st);
   return e == cudaSuccess ? SHAMPOO_OK : SHAMPOO_ECUDA;
@@ -224,9 +250,8 @@ int shampoo_adamw_load_moments(shampoo_adamw* c, const float* m, const float* v,
   if (!m || !v || !dash::aligned_to(m, 32) || !dash::aligned_to(v, 32)) return SHAMPOO_EINVAL;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (cudaMemsetAsync(ws, 0, sizeof(unsigned), st) != cudaSuccess) return SHAMPOO_ECUDA;
-  const int n = static_cast<int>(c->chunks.size());
-  if (n == 0) return SHAMPOO_OK;
-  dash::launch_load_moments(table(ws), n, std::min(n, c->load_blocks), static_cast<AdamwHeader*>(ws), m, v, st);
+  if (c->blocks == 0) return SHAMPOO_OK;
+  dash::launch_load_moments(table(c, ws), grid_for(warp_blocks(c), c->launch.load), static_cast<AdamwHeader*>(ws), m, v, st);
   return cudaGetLastError() == cudaSuccess ? SHAMPOO_OK : SHAMPOO_ECUDA;
 }
 
@@ -237,9 +262,8 @@ int shampoo_adamw_read_moments(shampoo_adamw* c, void* m, void* v, int dtype, vo
   if (!m || !v || (dtype != SHAMPOO_DTYPE_F32 && dtype != SHAMPOO_DTYPE_BF16) || !dash::aligned_to(m, 32) ||
       !dash::aligned_to(v, 32))
     return SHAMPOO_EINVAL;
-  const int n = static_cast<int>(c->chunks.size());
-  if (n == 0) return SHAMPOO_OK;
-  dash::launch_read_moments(table(ws), n, std::min(n, c->read_blocks), m, v, dtype, static_cast<cudaStream_t>(stream));
+  if (c->blocks == 0) return SHAMPOO_OK;
+  dash::launch_read_moments(table(c, ws), grid_for(warp_blocks(c), c->launch.read), m, v, dtype, static_cast<cudaStream_t>(stream));
   return cudaGetLastError() == cudaSuccess ? SHAMPOO_OK : SHAMPOO_ECUDA;
 }
 

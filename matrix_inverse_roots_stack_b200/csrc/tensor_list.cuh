@@ -161,11 +161,11 @@ __device__ __forceinline__ bool last_block(unsigned* ticket) {
 
 // Blocks of 'kernel' that fill the device, or a negative SHAMPOO_E* code.
 template <typename Kernel>
-int resident_blocks(Kernel kernel) {
+int resident_blocks(Kernel kernel, int threads = kListThreads, size_t smem = 0) {
   int dev = 0, sms = 0, per = 0;
   if (cudaGetDevice(&dev) != cudaSuccess ||
       cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
-      cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per, kernel, kListThreads, 0) != cudaSuccess || per < 1)
+      cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per, kernel, threads, smem) != cudaSuccess || per < 1)
     return SHAMPOO_ECUDA;
   return sms * per;
 }

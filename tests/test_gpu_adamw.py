@@ -123,9 +123,10 @@ def check_step(torch, opt, before, t, lr, coef=1.0, decay=0.1, lr_scale=1.0):
         p, m, v = oa.step(p0, g, m0, v0, t, b1, b2, eps, lr, decay, coef)
         # m: product and sum on one side, coef, product and sum on the other
         em = H * (2 * np.abs(b1 * m0) + 3 * np.abs((1 - b1) * coef * g)) * 1.01 + 2 * TINY
-        # v: at most five roundings of positive terms; its root half of that and one more
+        # v: at most five roundings of positive terms; its root half of that and the approximate square root's
+        # 2^-23; below fp32's normal range v counts as 0
         ev, r = 5 * H * v * 1.01 + 2 * TINY, np.sqrt(v)
-        er = 3.5 * H * r * 1.01 + np.sqrt(TINY) * (v < 1e-37)
+        er = np.where(v < 1.01 * 2.0 ** -126, r, 4.5 * H * r * 1.01)
         c1, c2 = 1 / (1 - b1 ** t), 1 / np.sqrt(1 - b2 ** t)
         den = r * c2 + eps
         ratio = np.abs(m * c1 / den)
