@@ -383,53 +383,57 @@ def _check_list(tensors, what, dtypes, device, like=None):
 
 class _TensorList:
     """What the operators over a list of tensors share: the library's list,
-    its workspace, and the streams it is used on."""
+    its workspace, and the streams it is used on.  A step is one launch of a
+    few microseconds, so what a call needs is looked up here once."""
 
     _destroy = None
 
     def _adopt(self, ctx, ws_bytes, owned):
         import torch
         self._ctx = ctx
+        self._cuda = torch.cuda
+        self._index = self.device.index
         self.ws = _workspace(ws_bytes, self.device)
-        self._ws_args = (_ptr(self.ws), self.ws.numel())
+        self._ws_at, self._ws_bytes = self.ws.data_ptr(), self.ws.numel()
         self._owned = [self.ws] + owned
         self._streams = {torch.cuda.current_stream(self.device).cuda_stream}
+        # the current stream's handle, without an object around it where torch offers that
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        self._current = raw if raw is not None else lambda index: torch.cuda.current_stream(index).cuda_stream
 
-    def _call(self, where, fn, args, stream, *passed):
-        """Run a library call on the list's device, on `stream` (default: that
-        device's current stream).  passed: the caller's tensors it works on."""
-        import torch
+    def _on(self, stream, *passed):
+        """The handle of `stream` (default: the current stream of the list's
+        device).  passed: the caller's tensors that the call works on."""
         if stream is None:
-            stream = torch.cuda.current_stream(self.device)
+            raw = self._current(self._index)
         elif stream.device != self.device:
             raise ValueError(f"the stream is on {stream.device}, the tensors are on {self.device}")
         else:
+            raw = stream.cuda_stream
             for t in passed:
-                t.record_stream(stream)
-        raw = stream.cuda_stream
+                if t is not None:
+                    t.record_stream(stream)
         if raw not in self._streams:
             # memory made here is not handed out again before this stream is done with it
             for t in self._owned:
-                t.record_stream(stream)
+                t.record_stream(self._cuda.current_stream(self.device) if stream is None else stream)
             self._streams.add(raw)
-        if torch.cuda.current_device() == self.device.index:
-            rc = fn(*args, ctypes.c_void_p(raw))
-        else:
-            with torch.cuda.device(self.device):
-                rc = fn(*args, ctypes.c_void_p(raw))
-        if rc != SHAMPOO_OK:
-            raise ShampooError(rc, where)
+        return raw
 
-    def _scalar(self, t, what):
-        import torch
-        if t.dtype != torch.float32 or t.numel() != 1 or t.device != self.device:
-            raise ValueError(f"{what} must be one fp32 value on {self.device}")
-        return _ptr(t)
+    def _run(self, name, *args):
+        """A library call, on the list's device."""
+        fn = getattr(_lib, name)
+        if self._cuda.current_device() == self._index:
+            rc = fn(*args)
+        else:
+            with self._cuda.device(self.device):
+                rc = fn(*args)
+        if rc != SHAMPOO_OK:
+            raise ShampooError(rc, name)
 
     def status(self, stream=None):
         """Synchronise and return (code, flags) of the last call."""
-        import torch
-        return read_status(self.ws, torch.cuda.current_stream(self.device) if stream is None else stream)
+        return read_status(self.ws, self._cuda.current_stream(self.device) if stream is None else stream)
 
     def __del__(self):
         ctx = getattr(self, "_ctx", None)
@@ -461,21 +465,22 @@ class GradClip(_TensorList):
         _check(load().shampoo_grads_init(ctypes.byref(ctx), arr, len(self.grads), ctypes.byref(nbytes)),
                "shampoo_grads_init")
         self.out = torch.zeros(2, dtype=torch.float32, device=self.device)
+        self._out_at = self.out.data_ptr()
         self._adopt(ctx, nbytes.value, [self.out])
-        self._call("shampoo_grads_bind", load().shampoo_grads_bind, (ctx, *self._ws_args), None)
+        self._run("shampoo_grads_bind", ctx, self._ws_at, self._ws_bytes, self._on(None))
         torch.cuda.current_stream(self.device).synchronize()  # ready for any stream
 
     def norm(self, max_norm=float("inf"), inv_scale=1.0, stream=None):
         """Fill and return :attr:`out`; the gradients are only read."""
-        self._call("shampoo_grad_norm", load().shampoo_grad_norm,
-                   (self._ctx, max_norm, inv_scale, _ptr(self.out), *self._ws_args), stream)
+        self._run("shampoo_grad_norm", self._ctx, max_norm, inv_scale, self._out_at, self._ws_at, self._ws_bytes,
+                  self._on(stream))
         return self.out
 
     def clip(self, max_norm, inv_scale=1.0, stream=None):
         """:meth:`norm`, then every gradient times coef, in place (zero where
         coef is NaN)."""
-        self._call("shampoo_grad_clip", load().shampoo_grad_clip,
-                   (self._ctx, max_norm, inv_scale, _ptr(self.out), *self._ws_args), stream)
+        self._run("shampoo_grad_clip", self._ctx, max_norm, inv_scale, self._out_at, self._ws_at, self._ws_bytes,
+                  self._on(stream))
         return self.out
 
 
@@ -562,7 +567,8 @@ class AdamW(_TensorList):
                                          ctypes.byref(elems)), "shampoo_adamw_init")
         self.moment_elems = elems.value
         self._adopt(ctx, nbytes.value, owned)
-        self._call("shampoo_adamw_bind", load().shampoo_adamw_bind, (ctx, steps_taken, *self._ws_args), None)
+        self._dtypes = {f32: DTYPE_F32, bf16: DTYPE_BF16}
+        self._run("shampoo_adamw_bind", ctx, steps_taken, self._ws_at, self._ws_bytes, self._on(None))
         torch.cuda.current_stream(dev).synchronize()  # ready for any stream
 
     def step(self, lr=1e-3, coef=None, step=0, stream=None):
@@ -571,25 +577,34 @@ class AdamW(_TensorList):
         the device that multiplies the gradients (``GradClip.out[1:]``); where
         it is not finite the step is not taken.  step: this step's number, or
         0 to continue the counter on the device."""
-        on_device = hasattr(lr, "data_ptr")
-        self._call("shampoo_adamw_step", load().shampoo_adamw_step,
-                   (self._ctx, step, 0.0 if on_device else lr, self._scalar(lr, "lr") if on_device else None,
-                    None if coef is None else self._scalar(coef, "coef"), *self._ws_args), stream,
-                   *([lr] if on_device else []), *([] if coef is None else [coef]))
+        lr_at = coef_at = None
+        if hasattr(lr, "data_ptr"):
+            lr, lr_at, held = 0.0, self._scalar(lr, "lr"), lr
+        else:
+            held = None
+        if coef is not None:
+            coef_at = self._scalar(coef, "coef")
+        self._run("shampoo_adamw_step", self._ctx, step, lr, lr_at, coef_at, self._ws_at, self._ws_bytes,
+                  self._on(stream, held, coef))
 
     def steps_taken(self, stream=None):
         """Synchronise and read the step counter."""
         t = ctypes.c_int(0)
-        fn = load().shampoo_adamw_steps_taken
-        self._call("shampoo_adamw_steps_taken", lambda *a: fn(*a, ctypes.byref(t)), (self._ctx, *self._ws_args),
-                   stream)
+        self._run("shampoo_adamw_steps_taken", self._ctx, self._ws_at, self._ws_bytes, self._on(stream),
+                  ctypes.byref(t))
         return t.value
 
-    def _flat(self, t, what, dtypes):
-        _check_list([t], what, dtypes, self.device)
-        if t.numel() != self.moment_elems:
-            raise ValueError(f"{what} has {t.numel()} elements, not {self.moment_elems}")
-        return _ptr(t)
+    def _scalar(self, t, what):
+        if t.dtype not in self._dtypes or self._dtypes[t.dtype] != DTYPE_F32 or t.numel() != 1 or \
+                t.device != self.device:
+            raise ValueError(f"{what} must be one fp32 value on {self.device}")
+        return t.data_ptr()
+
+    def _flat(self, t, what):
+        if t.dtype not in self._dtypes or t.numel() != self.moment_elems or not t.is_contiguous() or \
+                t.device != self.device:
+            raise ValueError(f"{what} must be {self.moment_elems} contiguous fp32 or bf16 values on {self.device}")
+        return t.data_ptr()
 
     def views(self, flat):
         """Each parameter's part of a flat tensor of moments, in its shape."""
@@ -607,16 +622,17 @@ class AdamW(_TensorList):
             m = torch.empty(self.moment_elems, dtype=dtype or torch.float32, device=self.device)
         if v is None:
             v = torch.empty(self.moment_elems, dtype=m.dtype, device=self.device)
+        m_at, v_at = self._flat(m, "m"), self._flat(v, "v")
         if v.dtype != m.dtype or (dtype is not None and m.dtype != dtype):
             raise ValueError("m and v must be of the one type asked for")
-        pm, pv = (self._flat(t, w, (torch.float32, torch.bfloat16)) for t, w in ((m, "m"), (v, "v")))
-        self._call("shampoo_adamw_read_moments", load().shampoo_adamw_read_moments,
-                   (self._ctx, pm, pv, _dtype_code(m), *self._ws_args), stream, m, v)
+        self._run("shampoo_adamw_read_moments", self._ctx, m_at, v_at, self._dtypes[m.dtype], self._ws_at,
+                  self._ws_bytes, self._on(stream, m, v))
         return m, v
 
     def load_moments(self, m, v, stream=None):
         """Set both moments from flat fp32 tensors (see :meth:`views`)."""
-        import torch
-        pm, pv = (self._flat(t, w, (torch.float32,)) for t, w in ((m, "m"), (v, "v")))
-        self._call("shampoo_adamw_load_moments", load().shampoo_adamw_load_moments,
-                   (self._ctx, pm, pv, *self._ws_args), stream, m, v)
+        m_at, v_at = self._flat(m, "m"), self._flat(v, "v")
+        if self._dtypes[m.dtype] != DTYPE_F32 or self._dtypes[v.dtype] != DTYPE_F32:
+            raise ValueError("moments are set from fp32 values")
+        self._run("shampoo_adamw_load_moments", self._ctx, m_at, v_at, self._ws_at, self._ws_bytes,
+                  self._on(stream, m, v))

@@ -360,18 +360,32 @@ __device__ __forceinline__ bool step_block(const TileDesc& t, int pt, int gt, in
       vs = *vs_at;
       rm.w[0] = rm.w[1] = rv.w[0] = rv.w[1] = 0;
     }
+    float x[8], y[8];
+    load8_strided(grad, i0, left, gt, x);
+    load8_strided(param, i0, left, pt, y);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      rg.w[j] = __float_as_uint(x[j]);
+      rp.w[j] = __float_as_uint(y[j]);
+    }
+    unsigned char bm[8], bv[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       const int i = i0 + 32 * j;
       const bool in = i < left;
-      rg.w[j] = __float_as_uint(in ? load1(grad, i, gt) : 0.0f);
-      rp.w[j] = __float_as_uint(in ? load1(param, i, pt) : 0.0f);
       if (kEight) {
-        rm.w[j >> 2] |= in ? static_cast<unsigned>(static_cast<uint8_t>(cm[i])) << (8 * (j & 3)) : 0u;
-        rv.w[j >> 2] |= in ? static_cast<unsigned>(static_cast<uint8_t>(cv[i])) << (8 * (j & 3)) : 0u;
+        bm[j] = in ? static_cast<unsigned char>(cm[i]) : 0;
+        bv[j] = in ? static_cast<unsigned char>(cv[i]) : 0;
       } else {
         rm.w[j] = in ? reinterpret_cast<const unsigned*>(cm)[i] : 0u;
         rv.w[j] = in ? reinterpret_cast<const unsigned*>(cv)[i] : 0u;
+      }
+    }
+    if (kEight) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        rm.w[j >> 2] |= static_cast<unsigned>(bm[j]) << (8 * (j & 3));
+        rv.w[j >> 2] |= static_cast<unsigned>(bv[j]) << (8 * (j & 3));
       }
     }
   }
@@ -851,24 +865,25 @@ __global__ void __launch_bounds__(kRingThreads, 1) adamw_mixed_kernel(const __gr
 // ---------------------------------------------------------------- moments in and out
 
 // From flat fp32 moments into the list's own: 8-bit tensors are rounded to
-// nearest, 32-bit ones copied.
+// nearest, 32-bit ones copied.  One block of threads to a tile, here and
+// below.
 __global__ void __launch_bounds__(kListThreads) load_moments_kernel(const AdamwTable table, AdamwHeader* hdr,
                                                                     const float* __restrict__ m_in,
                                                                     const float* __restrict__ v_in) {
   const int lane = threadIdx.x & 31;
-  int b = blockIdx.x * kListWarps + (threadIdx.x >> 5);
-  if (b >= table.n_blocks) return;
-  int at = first_tensor(table.first, table.n_tensors, b);
+  const AdamwTensorDev& t = table.tensors[first_tensor(table.first_tile, table.n_tensors, static_cast<int>(blockIdx.x))];
+  const long long tile0 = static_cast<long long>(static_cast<int>(blockIdx.x) - t.first_tile) * kTile;
   bool bad = false;
-  for (; b < table.n_blocks; b += gridDim.x * kListWarps) {
-    at = find_tensor(table.first, table.n_tensors, b, at);
-    const AdamwTensorDev& t = table.tensors[at];
-    const long long e0 = static_cast<long long>(b - t.first) * kQBlock;
+#pragma unroll
+  for (int w = 0; w < kTileBlocks / kListWarps; ++w) {
+    const long long e0 = tile0 + ((threadIdx.x >> 5) + w * kListWarps) * kQBlock;
+    if (e0 >= t.n) break;
+    const long long flat = static_cast<long long>(t.first) * kQBlock + e0;
     const int left = static_cast<int>(min(static_cast<long long>(kQBlock), t.n - e0));
     const bool vec = (t.flags & kFlagVec) && left == kQBlock;
     const int i0 = vec ? 8 * lane : lane;
-    const float* fm = m_in + static_cast<long long>(b) * kQBlock;
-    const float* fv = v_in + static_cast<long long>(b) * kQBlock;
+    const float* fm = m_in + flat;
+    const float* fv = v_in + flat;
     float m[8], v[8], r[8];
     if (vec) {
       Raw8 rm, rv;
@@ -956,18 +971,18 @@ __global__ void __launch_bounds__(kListThreads) read_moments_kernel(const AdamwT
                                                                     int dtype) {
   const int lane = threadIdx.x & 31;
   const size_t size = dtype == SHAMPOO_DTYPE_F32 ? 4 : 2;
-  int b = blockIdx.x * kListWarps + (threadIdx.x >> 5);
-  if (b >= table.n_blocks) return;
-  int at = first_tensor(table.first, table.n_tensors, b);
-  for (; b < table.n_blocks; b += gridDim.x * kListWarps) {
-    at = find_tensor(table.first, table.n_tensors, b, at);
-    const AdamwTensorDev& t = table.tensors[at];
-    const long long e0 = static_cast<long long>(b - t.first) * kQBlock;
+  const AdamwTensorDev& t = table.tensors[first_tensor(table.first_tile, table.n_tensors, static_cast<int>(blockIdx.x))];
+  const long long tile0 = static_cast<long long>(static_cast<int>(blockIdx.x) - t.first_tile) * kTile;
+#pragma unroll
+  for (int w = 0; w < kTileBlocks / kListWarps; ++w) {
+    const long long e0 = tile0 + ((threadIdx.x >> 5) + w * kListWarps) * kQBlock;
+    if (e0 >= t.n) break;
+    const long long flat = static_cast<long long>(t.first) * kQBlock + e0;
     const int left = static_cast<int>(min(static_cast<long long>(kQBlock), t.n - e0));
     const bool vec = (t.flags & kFlagVec) && left == kQBlock;
     const int i0 = 8 * lane;
-    char* om = static_cast<char*>(m_out) + size * kQBlock * b;
-    char* ov = static_cast<char*>(v_out) + size * kQBlock * b;
+    char* om = static_cast<char*>(m_out) + size * flat;
+    char* ov = static_cast<char*>(v_out) + size * flat;
     f32x2 m[4], v[4];
     if (t.flags & kFlagEight) {
       const uint8_t* cm = static_cast<const uint8_t*>(t.m) + e0;
@@ -1050,9 +1065,7 @@ int adamw_prepare(int bits, int stage_bytes, AdamwLaunch* out) {
                  : bits == 8 ? prepare(adamw8_kernel, done[1], out)
                              : prepare(adamw_mixed_kernel, done[2], out);
   if (rc) return rc;
-  out->load = resident_blocks(load_moments_kernel);
-  out->read = resident_blocks(read_moments_kernel);
-  return out->step < 0 || out->load < 0 || out->read < 0 ? SHAMPOO_ECUDA : SHAMPOO_OK;
+  return out->step < 0 ? SHAMPOO_ECUDA : SHAMPOO_OK;
 }
 
 void launch_adamw(const AdamwTable& t, const AdamwLaunch& l, int grid, AdamwHeader* hdr, const AdamwArgs& a,
@@ -1063,14 +1076,13 @@ void launch_adamw(const AdamwTable& t, const AdamwLaunch& l, int grid, AdamwHead
   prof_count_launch();
 }
 
-void launch_load_moments(const AdamwTable& t, int grid, AdamwHeader* hdr, const float* m, const float* v,
-                         cudaStream_t st) {
-  load_moments_kernel<<<grid, kListThreads, 0, st>>>(t, hdr, m, v);
+void launch_load_moments(const AdamwTable& t, AdamwHeader* hdr, const float* m, const float* v, cudaStream_t st) {
+  load_moments_kernel<<<t.n_tiles, kListThreads, 0, st>>>(t, hdr, m, v);
   prof_count_launch();
 }
 
-void launch_read_moments(const AdamwTable& t, int grid, void* m, void* v, int dtype, cudaStream_t st) {
-  read_moments_kernel<<<grid, kListThreads, 0, st>>>(t, m, v, dtype);
+void launch_read_moments(const AdamwTable& t, void* m, void* v, int dtype, cudaStream_t st) {
+  read_moments_kernel<<<t.n_tiles, kListThreads, 0, st>>>(t, m, v, dtype);
   prof_count_launch();
 }
 

@@ -5,9 +5,7 @@
 
 namespace dash {
 
-// One tensor of the list (tensors without elements are left out).  Its blocks
-// of kQBlock elements, the last one short or not, follow those of the tensor
-// before it in one count over the list.
+// One tensor of the list (tensors without elements are left out).
 struct AdamwTensorDev {
   void* param;
   const void* grad;
@@ -17,8 +15,8 @@ struct AdamwTensorDev {
   uint8_t* v_scale;
   void* copy;        // fp32 parameters may have a 16-bit copy written beside them, or null
   long long n;
-  int first;         // first block; kQBlock times it is the tensor's place in the flat moments
-  int first_tile;    // first tile of kTile elements, counted over the list in the same way
+  int first;         // first block, counted over the list; kQBlock times it is its place in the flat moments
+  int first_tile;    // first tile of kTile elements, likewise counted
   int flags;
   int index;         // in the caller's list
   float lr_scale, decay;
@@ -36,13 +34,11 @@ constexpr int kFlagBulk = 1 << 14;                              // and bulk copi
 constexpr int kTileBlocks = 16;
 constexpr int kTile = kTileBlocks * kQBlock;
 
-// The list on the device: 'first' and 'first_tile' of each tensor; the
-// records.
+// The list on the device: 'first_tile' of each tensor; the records.
 struct AdamwTable {
-  const int* first;
   const int* first_tile;
   const AdamwTensorDev* tensors;
-  int n_tensors, n_blocks, n_tiles;
+  int n_tensors, n_tiles;
 };
 
 // Start of the workspace: the status word, the blocks' arrival count, and the
@@ -72,10 +68,10 @@ struct AdamwArgs {
   const float* coef;       // null: 1
 };
 
-// How the kernels are launched on the current device: blocks that fill it
-// (step, load, read), and the step's shared memory.
+// How the step is launched on the current device: blocks that fill it, and
+// their shared memory.
 struct AdamwLaunch {
-  int step, load, read;
+  int step;
   int bits;                  // 32, 8, or 0 for both
   int stages, stride, smem;
 };
@@ -84,8 +80,7 @@ int adamw_stage_bytes(bool eight, int param_dtype, int grad_dtype);
 int adamw_prepare(int bits, int stage_bytes, AdamwLaunch* out);
 void launch_adamw(const AdamwTable& t, const AdamwLaunch& l, int grid, AdamwHeader* hdr, const AdamwArgs& a,
                   cudaStream_t st);
-void launch_load_moments(const AdamwTable& t, int grid, AdamwHeader* hdr, const float* m, const float* v,
-                         cudaStream_t st);
-void launch_read_moments(const AdamwTable& t, int grid, void* m, void* v, int dtype, cudaStream_t st);
+void launch_load_moments(const AdamwTable& t, AdamwHeader* hdr, const float* m, const float* v, cudaStream_t st);
+void launch_read_moments(const AdamwTable& t, void* m, void* v, int dtype, cudaStream_t st);
 
 }  // namespace dash

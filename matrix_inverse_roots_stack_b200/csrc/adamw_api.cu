@@ -13,13 +13,13 @@ using dash::AdamwTensorDev;
 
 struct shampoo_adamw {
   shampoo_adamw_hparams hp{};
-  std::vector<int> first, first_tile;    // of each tensor
+  std::vector<int> first_tile;           // of each tensor
   std::vector<AdamwTensorDev> tensors;
   AdamwHeader start{};         // header that bind uploads
   int bits = 32;               // of every tensor's moments, or 0
   int stage_bytes = 0;         // of a tile in shared memory, at most
   int64_t blocks = 0, tiles = 0;
-  size_t off_tiles = 0, off_tensors = 0, total = 0;  // workspace
+  size_t off_tensors = 0, total = 0;  // workspace
   const void* bound_ws = nullptr;
   dash::AdamwLaunch launch{};
 };
@@ -82,7 +82,6 @@ void add_tensor(shampoo_adamw* c, const shampoo_adamw_tensor& q, int index) {
   r.lr_scale = q.lr_scale;
   r.decay = q.weight_decay;
   c->bits = c->tensors.empty() || c->bits == q.state_bits ? q.state_bits : 0;
-  c->first.push_back(r.first);
   c->first_tile.push_back(r.first_tile);
   c->tensors.push_back(r);
   c->blocks += (q.n + dash::kQBlock - 1) / dash::kQBlock;
@@ -112,16 +111,9 @@ int check_bound(const shampoo_adamw* c, const void* ws, size_t ws_bytes) {
 
 AdamwTable table(const shampoo_adamw* c, const void* ws) {
   const char* w = static_cast<const char*>(ws);
-  return {reinterpret_cast<const int*>(w + kHeaderBytes), reinterpret_cast<const int*>(w + c->off_tiles),
-          reinterpret_cast<const AdamwTensorDev*>(w + c->off_tensors), static_cast<int>(c->tensors.size()),
-          static_cast<int>(c->blocks), static_cast<int>(c->tiles)};
+  return {reinterpret_cast<const int*>(w + kHeaderBytes), reinterpret_cast<const AdamwTensorDev*>(w + c->off_tensors),
+          static_cast<int>(c->tensors.size()), static_cast<int>(c->tiles)};
 }
-
-// Blocks of threads for so many pieces of work.
-int grid_for(int64_t pieces, int resident) {
-  return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(pieces, resident)));
-}
-int64_t warp_blocks(const shampoo_adamw* c) { return (c->blocks + dash::kListWarps - 1) / dash::kListWarps; }
 
 }  // namespace
 
@@ -169,8 +161,7 @@ int shampoo_adamw_init(shampoo_adamw** out, const shampoo_adamw_tensor* tensors,
     delete c;
     return SHAMPOO_EINVAL;
   }
-  c->off_tiles = kHeaderBytes + c->first.size() * sizeof(int);
-  c->off_tensors = (c->off_tiles + c->first_tile.size() * sizeof(int) + 255) / 256 * 256;
+  c->off_tensors = (kHeaderBytes + c->first_tile.size() * sizeof(int) + 255) / 256 * 256;
   c->total = c->off_tensors + c->tensors.size() * sizeof(AdamwTensorDev);
   *workspace_bytes = c->total;
   if (moment_elems) *moment_elems = c->blocks * dash::kQBlock;
@@ -200,9 +191,7 @@ int shampoo_adamw_bind(shampoo_adamw* c, int steps_taken, void* ws, size_t ws_by
   if (cudaMemcpyAsync(w, &c->start, sizeof(c->start), cudaMemcpyHostToDevice, st) != cudaSuccess)
     return SHAMPOO_ECUDA;
   if (!c->tensors.empty() &&
-      (cudaMemcpyAsync(w + kHeaderBytes, c->first.data(), c->first.size() * sizeof(int), cudaMemcpyHostToDevice,
-                       st) != cudaSuccess ||
-       cudaMemcpyAsync(w + c->off_tiles, c->first_tile.data(), c->first_tile.size() * sizeof(int),
+      (cudaMemcpyAsync(w + kHeaderBytes, c->first_tile.data(), c->first_tile.size() * sizeof(int),
                        cudaMemcpyHostToDevice, st) != cudaSuccess ||
        cudaMemcpyAsync(w + c->off_tensors, c->tensors.data(), c->tensors.size() * sizeof(AdamwTensorDev),
                        cudaMemcpyHostToDevice, st) != cudaSuccess))
@@ -237,7 +226,8 @@ int shampoo_adamw_step(shampoo_adamw* c, int step, float lr, const float* lr_dev
   a.lr_device = lr_device;
   a.coef = coef;
   const int slot = dash::prof_begin(dash::kProfAdam, st);
-  dash::launch_adamw(table(c, ws), c->launch, grid_for(c->tiles, c->launch.step), static_cast<AdamwHeader*>(ws), a, st);
+  const int grid = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(c->tiles, c->launch.step)));
+  dash::launch_adamw(table(c, ws), c->launch, grid, static_cast<AdamwHeader*>(ws), a, st);
   const cudaError_t e = cudaGetLastError();
   dash::prof_end(slot, st);
   return e == cudaSuccess ? SHAMPOO_OK : SHAMPOO_ECUDA;
@@ -251,7 +241,7 @@ int shampoo_adamw_load_moments(shampoo_adamw* c, const float* m, const float* v,
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (cudaMemsetAsync(ws, 0, sizeof(unsigned), st) != cudaSuccess) return SHAMPOO_ECUDA;
   if (c->blocks == 0) return SHAMPOO_OK;
-  dash::launch_load_moments(table(c, ws), grid_for(warp_blocks(c), c->launch.load), static_cast<AdamwHeader*>(ws), m, v, st);
+  dash::launch_load_moments(table(c, ws), static_cast<AdamwHeader*>(ws), m, v, st);
   return cudaGetLastError() == cudaSuccess ? SHAMPOO_OK : SHAMPOO_ECUDA;
 }
 
@@ -263,7 +253,7 @@ int shampoo_adamw_read_moments(shampoo_adamw* c, void* m, void* v, int dtype, vo
       !dash::aligned_to(v, 32))
     return SHAMPOO_EINVAL;
   if (c->blocks == 0) return SHAMPOO_OK;
-  dash::launch_read_moments(table(c, ws), grid_for(warp_blocks(c), c->launch.read), m, v, dtype, static_cast<cudaStream_t>(stream));
+  dash::launch_read_moments(table(c, ws), m, v, dtype, static_cast<cudaStream_t>(stream));
   return cudaGetLastError() == cudaSuccess ? SHAMPOO_OK : SHAMPOO_ECUDA;
 }
 

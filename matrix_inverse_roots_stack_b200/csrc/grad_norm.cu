@@ -27,10 +27,12 @@ constexpr int kTypeMask = 15;
 struct NormHeader {
   unsigned status;  // first word: the status word
   unsigned ticket;
+  unsigned next;    // shares taken in the running call, beyond the first of each block
 };
 constexpr size_t kHeaderBytes = 256;
 constexpr int kSteps = 4;  // warp steps in flight: a chunk is kSteps x kListWarps x 256 elements
 constexpr int kChunk = kSteps * kListWarps * kQBlock;
+constexpr int kTurns = 8;  // shares for each resident block in a long list, or up to twice that
 
 __device__ __forceinline__ void add_squares(const float* x, double* acc) {
 #pragma unroll
@@ -57,40 +59,54 @@ __device__ __forceinline__ double block_sum(double x) {
 // The squares are formed and added in fp64: the square of any finite fp32
 // value is exact and in range there, so neither small nor large gradients
 // are lost, and the result is not finite exactly when an element is not.
-// Each block adds a fixed set of chunks and the last one to finish adds the
-// blocks' sums, so that the order, and with it the result, is the same on
-// every call.  Chunks are taken from the end: what the L2 cache still holds
-// afterwards is the front of the list, where the next pass starts.
+//
+// A share is 'rounds' chunks, a grid's width apart, so that blocks that run
+// side by side read side by side.  A block adds up a share in a fixed order,
+// wherever it runs, and the last block to finish adds the shares' sums: the
+// result is the same on every call, while the blocks take shares as they come
+// (SMs differ in how far from memory they are).  Chunks are counted from the
+// end, because what the L2 cache still holds afterwards is then the front of
+// the list, where the pass that follows starts.
 __global__ void __launch_bounds__(kListThreads) grad_norm_kernel(const GradChunk* __restrict__ chunks, int n_chunks,
-                                                                 NormHeader* hdr, double* partial, double max_norm,
-                                                                 double inv_scale, float* out) {
+                                                                 int shares, int rounds, NormHeader* hdr, double* partial,
+                                                                 double max_norm, double inv_scale, float* out) {
+  __shared__ int taken;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  double acc[2] = {0.0, 0.0};
-  for (int k = n_chunks - 1 - static_cast<int>(blockIdx.x); k >= 0; k -= gridDim.x) {
-    const GradChunk c = chunks[k];
-    const int type = c.flags & kTypeMask;
-    if ((c.flags & kVec) && c.count == kChunk) {
-      Raw8 r[kSteps];
+  for (int p = blockIdx.x; p < shares;) {
+    unsigned next = 0;  // looked at behind the share
+    if (threadIdx.x == 0) next = atomicAdd(&hdr->next, 1u);
+    double acc[2] = {0.0, 0.0};
+    const int width = gridDim.x, first = p / width * (width * rounds) + p % width;
+    for (int j = 0, k = n_chunks - 1 - first; j < rounds && k >= 0; ++j, k -= width) {
+      const GradChunk c = chunks[k];
+      const int type = c.flags & kTypeMask;
+      if ((c.flags & kVec) && c.count == kChunk) {
+        Raw8 r[kSteps];
 #pragma unroll
-      for (int s = 0; s < kSteps; ++s) load8(c.grad, (s * kListWarps + warp) * 32 + lane, type, r[s]);
+        for (int s = 0; s < kSteps; ++s) load8(c.grad, (s * kListWarps + warp) * 32 + lane, type, r[s]);
 #pragma unroll
-      for (int s = 0; s < kSteps; ++s) {
-        float x[8];
-        widen8(r[s], type, x);
-        add_squares(x, acc);
-      }
-    } else {
-      for (int i = threadIdx.x; i < c.count; i += kListThreads) {
-        const double d = load1(c.grad, i, type);
-        acc[0] = fma(d, d, acc[0]);
+        for (int s = 0; s < kSteps; ++s) {
+          float x[8];
+          widen8(r[s], type, x);
+          add_squares(x, acc);
+        }
+      } else {
+        for (int b = warp * kQBlock; b < c.count; b += kListWarps * kQBlock) {
+          float x[8];
+          load8_strided(c.grad, b + lane, c.count, type, x);
+          add_squares(x, acc);
+        }
       }
     }
+    if (threadIdx.x == 0) taken = static_cast<int>(gridDim.x + next);
+    const double sum = block_sum(acc[0] + acc[1]);  // with barriers: 'taken' is there
+    if (threadIdx.x == 0) partial[p] = sum;
+    p = taken;
+    __syncthreads();
   }
-  const double sum = block_sum(acc[0] + acc[1]);
-  if (threadIdx.x == 0) partial[blockIdx.x] = sum;
   if (!last_block(&hdr->ticket)) return;
   double t = 0.0;
-  for (int i = threadIdx.x; i < static_cast<int>(gridDim.x); i += kListThreads) t += __ldcg(partial + i);
+  for (int i = threadIdx.x; i < shares; i += kListThreads) t += __ldcg(partial + i);
   t = block_sum(t);
   if (threadIdx.x == 0) {
     const double norm = sqrt(t) * inv_scale;
@@ -98,35 +114,39 @@ __global__ void __launch_bounds__(kListThreads) grad_norm_kernel(const GradChunk
     out[0] = static_cast<float>(norm);
     out[1] = ok ? static_cast<float>((norm > max_norm ? max_norm / norm : 1.0) * inv_scale) : __int_as_float(0x7fffffff);
     hdr->status = ok ? 0u : kStatusNonFinite;
+    hdr->next = 0;
   }
 }
 
 // g <- coef g; a coefficient of 1 leaves the gradients unread, one that is
-// not finite sets them to zero.
-__global__ void __launch_bounds__(kListThreads) grad_clip_kernel(const GradChunk* __restrict__ chunks, int n_chunks,
+// not finite sets them to zero.  One block of threads to a chunk.
+__global__ void __launch_bounds__(kListThreads) grad_clip_kernel(const GradChunk* __restrict__ chunks,
                                                                  const float* __restrict__ out) {
   const float coef = out[1];
   if (coef == 1.0f) return;
   const bool zero = not_finite(coef);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  for (int k = blockIdx.x; k < n_chunks; k += gridDim.x) {
-    const GradChunk c = chunks[k];
-    const int type = c.flags & kTypeMask;
-    if ((c.flags & kVec) && c.count == kChunk) {
-      Raw8 r[kSteps];
+  const GradChunk c = chunks[blockIdx.x];
+  const int type = c.flags & kTypeMask;
+  if ((c.flags & kVec) && c.count == kChunk) {
+    Raw8 r[kSteps];
 #pragma unroll
-      for (int s = 0; s < kSteps; ++s) load8(c.grad, (s * kListWarps + warp) * 32 + lane, type, r[s]);
+    for (int s = 0; s < kSteps; ++s) load8(c.grad, (s * kListWarps + warp) * 32 + lane, type, r[s]);
 #pragma unroll
-      for (int s = 0; s < kSteps; ++s) {
-        float x[8];
-        widen8(r[s], type, x);
+    for (int s = 0; s < kSteps; ++s) {
+      float x[8];
+      widen8(r[s], type, x);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) x[j] = zero ? 0.0f : x[j] * coef;
-        store8(c.grad, (s * kListWarps + warp) * 32 + lane, type, x);
-      }
-    } else {
-      for (int i = threadIdx.x; i < c.count; i += kListThreads)
-        store1(c.grad, i, type, zero ? 0.0f : load1(c.grad, i, type) * coef);
+      for (int j = 0; j < 8; ++j) x[j] = zero ? 0.0f : x[j] * coef;
+      store8(c.grad, (s * kListWarps + warp) * 32 + lane, type, x);
+    }
+  } else {
+    for (int b = warp * kQBlock; b < c.count; b += kListWarps * kQBlock) {
+      float x[8];
+      load8_strided(c.grad, b + lane, c.count, type, x);
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (b + lane + 32 * j < c.count) store1(c.grad, b + lane + 32 * j, type, zero ? 0.0f : x[j] * coef);
     }
   }
 }
@@ -138,12 +158,12 @@ struct shampoo_grads {
   std::vector<dash::GradChunk> chunks;
   size_t off_partial = 0, total = 0;
   const void* bound_ws = nullptr;
-  int norm_blocks = 0, clip_blocks = 0;
+  int shares = 0, rounds = 1, grid = 1;
 };
 
 namespace {
 
-constexpr int kMaxBlocks = 8192;  // partial sums kept in the workspace
+constexpr int kMaxShares = 1 << 15;  // partial sums kept in the workspace
 
 int norm_pass(shampoo_grads* c, float max_norm, float inv_scale, float* out, void* ws, size_t ws_bytes, void* stream,
               bool clip) {
@@ -154,14 +174,13 @@ int norm_pass(shampoo_grads* c, float max_norm, float inv_scale, float* out, voi
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const auto* table = reinterpret_cast<const dash::GradChunk*>(w + dash::kHeaderBytes);
   const int n = static_cast<int>(c->chunks.size());
-  const int grid = std::max(1, std::min(n, c->norm_blocks));
-  dash::grad_norm_kernel<<<grid, dash::kListThreads, 0, st>>>(
-      table, n, reinterpret_cast<dash::NormHeader*>(w), reinterpret_cast<double*>(w + c->off_partial), max_norm,
+  dash::grad_norm_kernel<<<c->grid, dash::kListThreads, 0, st>>>(
+      table, n, c->shares, c->rounds, reinterpret_cast<dash::NormHeader*>(w), reinterpret_cast<double*>(w + c->off_partial), max_norm,
       inv_scale, out);
   dash::prof_count_launch();
   if (cudaGetLastError() != cudaSuccess) return SHAMPOO_ECUDA;
   if (clip && n > 0) {
-    dash::grad_clip_kernel<<<std::min(n, c->clip_blocks), dash::kListThreads, 0, st>>>(table, n, out);
+    dash::grad_clip_kernel<<<n, dash::kListThreads, 0, st>>>(table, out);
     dash::prof_count_launch();
     if (cudaGetLastError() != cudaSuccess) return SHAMPOO_ECUDA;
   }
@@ -204,7 +223,7 @@ int shampoo_grads_init(shampoo_grads** out, const shampoo_grad* grads, int n_gra
   }
   const size_t table = (c->chunks.size() * sizeof(dash::GradChunk) + 255) / 256 * 256;
   c->off_partial = dash::kHeaderBytes + table;
-  c->total = c->off_partial + kMaxBlocks * sizeof(double);
+  c->total = c->off_partial + kMaxShares * sizeof(double);
   *workspace_bytes = c->total;
   *out = c;
   return SHAMPOO_OK;
@@ -218,10 +237,14 @@ int shampoo_grads_bind(shampoo_grads* c, void* ws, size_t ws_bytes, void* stream
   if (cudaStreamIsCapturing(st, &cap) != cudaSuccess) return SHAMPOO_ECUDA;
   if (cap != cudaStreamCaptureStatusNone) return SHAMPOO_EINVAL;
   c->bound_ws = nullptr;
-  const int nb = dash::resident_blocks(dash::grad_norm_kernel), cb = dash::resident_blocks(dash::grad_clip_kernel);
-  if (nb < 0 || cb < 0) return SHAMPOO_ECUDA;
-  c->norm_blocks = std::min(nb, kMaxBlocks);
-  c->clip_blocks = cb;
+  const int blocks = dash::resident_blocks(dash::grad_norm_kernel);
+  if (blocks < 0) return SHAMPOO_ECUDA;
+  const int n = static_cast<int>(c->chunks.size());
+  c->grid = std::max(1, std::min({n, blocks, kMaxShares / (2 * dash::kTurns)}));
+  c->rounds = std::max(1, n / (dash::kTurns * c->grid));
+  // whole groups of grid x rounds chunks, the last one short; with one round, a chunk to a share
+  const int group = c->grid * c->rounds;
+  c->shares = c->rounds == 1 ? n : (n + group - 1) / group * c->grid;
   if (cudaMemsetAsync(ws, 0, dash::kHeaderBytes, st) != cudaSuccess) return SHAMPOO_ECUDA;
   if (!c->chunks.empty() &&
       cudaMemcpyAsync(static_cast<char*>(ws) + dash::kHeaderBytes, c->chunks.data(),

@@ -129,6 +129,24 @@ __device__ __forceinline__ void store8(void* base, int i, int dtype, const float
   }
 }
 
+// Eight elements i, i + 32, ..., those below n, of a buffer with no more than
+// its type's alignment; the others are 0.  The loads leave together: nothing
+// is converted between them.
+__device__ __forceinline__ void load8_strided(const void* base, int i, int n, int dtype, float* x) {
+  unsigned w[8];
+  if (dtype == SHAMPOO_DTYPE_F32) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) w[j] = i + 32 * j < n ? static_cast<const unsigned*>(base)[i + 32 * j] : 0u;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) x[j] = __uint_as_float(w[j]);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) w[j] = i + 32 * j < n ? static_cast<const unsigned short*>(base)[i + 32 * j] : 0u;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) x[j] = widen(static_cast<unsigned short>(w[j]), dtype);
+  }
+}
+
 // Scalar path: element i of a buffer with no more than its type's alignment.
 __device__ __forceinline__ float load1(const void* base, int i, int dtype) {
   if (dtype == SHAMPOO_DTYPE_F32) return static_cast<const float*>(base)[i];
