@@ -13,7 +13,10 @@
 // that are taken off the warps that compute (adamw_step).
 //
 // The moments' products and sums are rounded one by one (no contraction), so
-// that their 8-bit codes do not depend on how a compiler fuses them.
+// that their 8-bit codes do not depend on how a compiler fuses them.  Packed
+// products and sums are fused by the assembler even where each asks for its
+// own rounding, so the sums are written as a b + c with a 1 that it does not
+// know to be one (AdamwArgs::one).
 #include <atomic>
 
 #include "adamw.cuh"
@@ -38,11 +41,6 @@ __device__ __forceinline__ float high(f32x2 a) { return __uint_as_float(static_c
 __device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b) {
   f32x2 r;
   asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ f32x2 add2(f32x2 a, f32x2 b) {
-  f32x2 r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
   return r;
 }
 __device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
@@ -420,8 +418,8 @@ __device__ __forceinline__ bool step_block(const TileDesc& t, int pt, int gt, in
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
     const f32x2 gs2 = mul2(g[j], both(k.coef));
-    m[j] = add2(mul2(m[j], pair(args.beta1)), mul2(gs2, pair(args.om1)));
-    v[j] = add2(mul2(v[j], pair(args.beta2)), mul2(mul2(gs2, pair(args.om2)), gs2));
+    m[j] = fma2(mul2(m[j], pair(args.beta1)), pair(args.one), mul2(gs2, pair(args.om1)));
+    v[j] = fma2(mul2(v[j], pair(args.beta2)), pair(args.one), mul2(mul2(gs2, pair(args.om2)), gs2));
     r[j] = kEight ? root2(v[j]) : pack2(root(low(v[j])), root(high(v[j])));
     const f32x2 den = fma2(r[j], both(k.d1), both(k.d0));
     const f32x2 ratio = mul2(m[j], pack2(reciprocal(low(den)), reciprocal(high(den))));

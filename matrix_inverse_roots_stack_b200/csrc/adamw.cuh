@@ -56,6 +56,7 @@ struct AdamwHeader {
 struct AdamwArgs {
   // beta, and 1 - beta, as pairs of one value: operands of the packed products, read from the constant bank
   float2 beta1, om1, beta2, om2;
+  float2 one;            // 1, not known as such when the kernel is compiled
   float eps;
   unsigned seed_lo, seed_hi;
   int step;              // > 0: take this step number and the values below; 0: the header's next

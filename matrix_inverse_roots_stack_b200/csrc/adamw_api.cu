@@ -211,6 +211,7 @@ int shampoo_adamw_step(shampoo_adamw* c, int step, float lr, const float* lr_dev
   a.beta2 = make_float2(c->hp.beta2, c->hp.beta2);
   a.om1 = make_float2(1.0f - c->hp.beta1, 1.0f - c->hp.beta1);
   a.om2 = make_float2(1.0f - c->hp.beta2, 1.0f - c->hp.beta2);
+  a.one = make_float2(1.0f, 1.0f);
   a.eps = c->hp.adam_eps;
   a.seed_lo = static_cast<unsigned>(c->hp.seed);
   a.seed_hi = static_cast<unsigned>(c->hp.seed >> 32);
