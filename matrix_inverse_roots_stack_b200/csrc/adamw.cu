@@ -310,18 +310,15 @@ __device__ __forceinline__ bool step_block(const TileDesc& t, int pt, int gt, in
   const int lane = threadIdx.x & 31;
   const int ct = (t.flags >> kCopyShift) & 15;
   const int left = vec ? kQBlock : min(kQBlock, t.left - at);
-  char* param = t.param + at * (pt == SHAMPOO_DTYPE_F32 ? 4 : 2);
-  const char* grad = t.grad + at * (gt == SHAMPOO_DTYPE_F32 ? 4 : 2);
-  char* copy = t.copy ? t.copy + 2 * at : nullptr;
-  char* cm = t.m + at * (kEight ? 1 : 4);
-  char* cv = t.v + at * (kEight ? 1 : 4);
-  uint8_t* ms_at = t.m_scale + (at >> 8);
-  uint8_t* vs_at = t.v_scale + (at >> 8);
-  const float neg_lr = t.neg_lr, decay = t.decay;
-  const unsigned key = t.key, elem = t.elem + at;
   // this lane's elements: 8 lane + j of the block, or lane + 32 j
   constexpr int stride = vec ? 1 : 32;
   const int i0 = vec ? 8 * lane : lane;
+
+  // where the block lies (of no use to kStaged, which reads shared memory)
+  const char* grad = t.grad + at * (gt == SHAMPOO_DTYPE_F32 ? 4 : 2);
+  const char* from = t.param + at * (pt == SHAMPOO_DTYPE_F32 ? 4 : 2);
+  const char* m_from = t.m + at * (kEight ? 1 : 4);
+  const char* v_from = t.v + at * (kEight ? 1 : 4);
 
   Raw8 rp, rg, rm, rv;
   f32x2 m[4], v[4], g[4], p[4], r[4];
@@ -343,24 +340,24 @@ __device__ __forceinline__ bool step_block(const TileDesc& t, int pt, int gt, in
   } else if (kAccess == kVector) {
     load8(grad, lane, gt, rg);
     if (kEight) {
-      const uint2 qm = *(reinterpret_cast<const uint2*>(cm) + lane), qv = *(reinterpret_cast<const uint2*>(cv) + lane);
+      const uint2 qm = *(reinterpret_cast<const uint2*>(m_from) + lane), qv = *(reinterpret_cast<const uint2*>(v_from) + lane);
       rm.w[0] = qm.x, rm.w[1] = qm.y, rv.w[0] = qv.x, rv.w[1] = qv.y;
-      ms = *ms_at;
-      vs = *vs_at;
+      ms = t.m_scale[at >> 8];
+      vs = t.v_scale[at >> 8];
     } else {
-      load8(cm, lane, SHAMPOO_DTYPE_F32, rm);
-      load8(cv, lane, SHAMPOO_DTYPE_F32, rv);
+      load8(m_from, lane, SHAMPOO_DTYPE_F32, rm);
+      load8(v_from, lane, SHAMPOO_DTYPE_F32, rv);
     }
-    load8(param, lane, pt, rp);
+    load8(from, lane, pt, rp);
   } else {
     if (kEight) {
-      ms = *ms_at;
-      vs = *vs_at;
+      ms = t.m_scale[at >> 8];
+      vs = t.v_scale[at >> 8];
       rm.w[0] = rm.w[1] = rv.w[0] = rv.w[1] = 0;
     }
     float x[8], y[8];
     load8_strided(grad, i0, left, gt, x);
-    load8_strided(param, i0, left, pt, y);
+    load8_strided(from, i0, left, pt, y);
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       rg.w[j] = __float_as_uint(x[j]);
@@ -372,11 +369,11 @@ __device__ __forceinline__ bool step_block(const TileDesc& t, int pt, int gt, in
       const int i = i0 + 32 * j;
       const bool in = i < left;
       if (kEight) {
-        bm[j] = in ? static_cast<unsigned char>(cm[i]) : 0;
-        bv[j] = in ? static_cast<unsigned char>(cv[i]) : 0;
+        bm[j] = in ? static_cast<unsigned char>(m_from[i]) : 0;
+        bv[j] = in ? static_cast<unsigned char>(v_from[i]) : 0;
       } else {
-        rm.w[j] = in ? reinterpret_cast<const unsigned*>(cm)[i] : 0u;
-        rv.w[j] = in ? reinterpret_cast<const unsigned*>(cv)[i] : 0u;
+        rm.w[j] = in ? reinterpret_cast<const unsigned*>(m_from)[i] : 0u;
+        rv.w[j] = in ? reinterpret_cast<const unsigned*>(v_from)[i] : 0u;
       }
     }
     if (kEight) {
@@ -423,7 +420,7 @@ __device__ __forceinline__ bool step_block(const TileDesc& t, int pt, int gt, in
     r[j] = kEight ? root2(v[j]) : pack2(root(low(v[j])), root(high(v[j])));
     const f32x2 den = fma2(r[j], both(k.d1), both(k.d0));
     const f32x2 ratio = mul2(m[j], pack2(reciprocal(low(den)), reciprocal(high(den))));
-    p[j] = fma2(both(neg_lr), fma2(both(decay), p[j], ratio), p[j]);
+    p[j] = fma2(both(t.neg_lr), fma2(both(t.decay), p[j], ratio), p[j]);
   }
   if (!vec) {  // nothing behind the tensor's end counts
 #pragma unroll
@@ -445,70 +442,18 @@ __device__ __forceinline__ bool step_block(const TileDesc& t, int pt, int gt, in
 
   unsigned h[8];
   if (kEight || pt == SHAMPOO_DTYPE_BF16) {
-    const unsigned x0 = (elem + i0) * kWeyl + key;
+    const unsigned x0 = (t.elem + at + i0) * kWeyl + t.key;
 #pragma unroll
     for (int j = 0; j < 8; ++j) h[j] = draw_bits(x0 + static_cast<unsigned>(stride * j) * kWeyl);
   }
 
-  if (kEight) {
-    mmax = warp_max(mmax);
-    rmax = warp_max(rmax);
-    const M8Scale mi(mmax);
-    const V8Scale vi(rmax);
-    const f32x2 mu = both(mi.inverse()), vu = both(vi.inverse());
-    unsigned a[8], b[8];
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const f32x2 x = mul2(mul2(m[j / 2], mu), both(kM8Down)), y = mul2(mul2(r[j / 2], vu), both(kV8Down));
-      const float xm = j & 1 ? high(x) : low(x), xr = j & 1 ? high(y) : low(y);
-      const float mj = j & 1 ? high(m[j / 2]) : low(m[j / 2]);
-      a[j] = m8_code(__float_as_uint(xm), mj, __byte_perm(h[j], 0, 0x4324));
-      b[j] = v8_code(__float_as_uint(xr), __byte_perm(h[j], 0, 0x4104));
-    }
-    const uint2 am = make_uint2(top_bytes(a[0], a[1], a[2], a[3]), top_bytes(a[4], a[5], a[6], a[7]));
-    uint2 bv = make_uint2(top_bytes(b[0], b[1], b[2], b[3]), top_bytes(b[4], b[5], b[6], b[7]));
-    if (zero_bytes(bv.x) | zero_bytes(bv.y)) {
-      bv.x = v8_floor(bv.x, r);
-      bv.y = v8_floor(bv.y, r + 2);
-    }
-    if (kAccess == kStaged) {
-      if (lane == 0) most[at >> 8] = make_float2(mmax, rmax);
-    } else if (lane == 0) {
-      *ms_at = mi.byte(mmax);
-      *vs_at = vi.byte(rmax);
-    }
-    if (vec) {
-      *(reinterpret_cast<uint2*>(cm) + lane) = am;
-      *(reinterpret_cast<uint2*>(cv) + lane) = bv;
-    } else {
-#pragma unroll
-      for (int j = 0; j < 8; ++j)
-        if (i0 + 32 * j < left) {
-          cm[i0 + 32 * j] = static_cast<char>((j < 4 ? am.x : am.y) >> (8 * (j & 3)));
-          cv[i0 + 32 * j] = static_cast<char>((j < 4 ? bv.x : bv.y) >> (8 * (j & 3)));
-        }
-    }
-  } else if (vec) {
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      rm.w[2 * j] = __float_as_uint(low(m[j])), rm.w[2 * j + 1] = __float_as_uint(high(m[j]));
-      rv.w[2 * j] = __float_as_uint(low(v[j])), rv.w[2 * j + 1] = __float_as_uint(high(v[j]));
-    }
-    store32B(reinterpret_cast<float*>(cm) + 8 * lane, rm.w);
-    store32B(reinterpret_cast<float*>(cv) + 8 * lane, rv.w);
-  } else {
-#pragma unroll
-    for (int j = 0; j < 8; ++j)
-      if (i0 + 32 * j < left) {
-        reinterpret_cast<float*>(cm)[i0 + 32 * j] = j & 1 ? high(m[j / 2]) : low(m[j / 2]);
-        reinterpret_cast<float*>(cv)[i0 + 32 * j] = j & 1 ? high(v[j / 2]) : low(v[j / 2]);
-      }
-  }
-
+  // the parameter leaves first: its registers are free for the codes
   float y[8];
 #pragma unroll
   for (int j = 0; j < 4; ++j) y[2 * j] = low(p[j]), y[2 * j + 1] = high(p[j]);
+  char* param = t.param + at * (pt == SHAMPOO_DTYPE_F32 ? 4 : 2);
   if (pt == SHAMPOO_DTYPE_F32) {
+    char* copy = t.copy ? t.copy + 2 * at : nullptr;
     if (vec) {
       store8(param, lane, SHAMPOO_DTYPE_F32, y);
       if (copy) store8(copy, lane, ct, y);
@@ -539,6 +484,64 @@ __device__ __forceinline__ bool step_block(const TileDesc& t, int pt, int gt, in
         if (i0 + 32 * j < left) reinterpret_cast<unsigned short*>(param)[i0 + 32 * j] = static_cast<unsigned short>(w[j] >> 16);
     }
   }
+
+  char* cm = t.m + at * (kEight ? 1 : 4);
+  char* cv = t.v + at * (kEight ? 1 : 4);
+  if (kEight) {
+    mmax = warp_max(mmax);
+    rmax = warp_max(rmax);
+    const M8Scale mi(mmax);
+    const V8Scale vi(rmax);
+    const f32x2 mu = both(mi.inverse()), vu = both(vi.inverse());
+    unsigned a[8], b[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const f32x2 x = mul2(mul2(m[j / 2], mu), both(kM8Down)), y = mul2(mul2(r[j / 2], vu), both(kV8Down));
+      const float xm = j & 1 ? high(x) : low(x), xr = j & 1 ? high(y) : low(y);
+      const float mj = j & 1 ? high(m[j / 2]) : low(m[j / 2]);
+      a[j] = m8_code(__float_as_uint(xm), mj, __byte_perm(h[j], 0, 0x4324));
+      b[j] = v8_code(__float_as_uint(xr), __byte_perm(h[j], 0, 0x4104));
+    }
+    const uint2 am = make_uint2(top_bytes(a[0], a[1], a[2], a[3]), top_bytes(a[4], a[5], a[6], a[7]));
+    uint2 bv = make_uint2(top_bytes(b[0], b[1], b[2], b[3]), top_bytes(b[4], b[5], b[6], b[7]));
+    if (zero_bytes(bv.x) | zero_bytes(bv.y)) {
+      bv.x = v8_floor(bv.x, r);
+      bv.y = v8_floor(bv.y, r + 2);
+    }
+    if (kAccess == kStaged) {
+      if (lane == 0) most[at >> 8] = make_float2(mmax, rmax);
+    } else if (lane == 0) {
+      t.m_scale[at >> 8] = mi.byte(mmax);
+      t.v_scale[at >> 8] = vi.byte(rmax);
+    }
+    if (vec) {
+      *(reinterpret_cast<uint2*>(cm) + lane) = am;
+      *(reinterpret_cast<uint2*>(cv) + lane) = bv;
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (i0 + 32 * j < left) {
+          cm[i0 + 32 * j] = static_cast<char>((j < 4 ? am.x : am.y) >> (8 * (j & 3)));
+          cv[i0 + 32 * j] = static_cast<char>((j < 4 ? bv.x : bv.y) >> (8 * (j & 3)));
+        }
+    }
+  } else if (vec) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      rm.w[2 * j] = __float_as_uint(low(m[j])), rm.w[2 * j + 1] = __float_as_uint(high(m[j]));
+      rv.w[2 * j] = __float_as_uint(low(v[j])), rv.w[2 * j + 1] = __float_as_uint(high(v[j]));
+    }
+    store32B(reinterpret_cast<float*>(cm) + 8 * lane, rm.w);
+    store32B(reinterpret_cast<float*>(cv) + 8 * lane, rv.w);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (i0 + 32 * j < left) {
+        reinterpret_cast<float*>(cm)[i0 + 32 * j] = j & 1 ? high(m[j / 2]) : low(m[j / 2]);
+        reinterpret_cast<float*>(cv)[i0 + 32 * j] = j & 1 ? high(v[j / 2]) : low(v[j / 2]);
+      }
+  }
+
   return bad;
 }
 
@@ -605,7 +608,7 @@ __device__ __noinline__ bool step_direct(const TileDesc& t, int at, const AdamwA
 }
 
 // One block of threads an SM.  One of its warps fetches tiles of 16 blocks
-// with bulk copies into a ring of stages in shared memory, ahead of the 15
+// with bulk copies into a ring of stages in shared memory, ahead of the 19
 // that compute.  It also forms and writes a finished tile's new scales: a byte
 // for every block, written by its own warp, cost 7 to 10% of the step.  A tile
 // that bulk copies cannot fetch (a tensor's short end, or other alignment) is
@@ -614,7 +617,7 @@ __device__ __noinline__ bool step_direct(const TileDesc& t, int at, const AdamwA
 //
 // Long lists are dealt out from a counter, since SMs differ in how far from
 // memory they are: with equal parts 32-bit steps took 10% longer.  See Deal.
-constexpr int kRingWarps = 15;  // and the fetching one: 4 to a scheduler, 128 registers a thread
+constexpr int kRingWarps = 19;  // and the fetching one: 5 to a scheduler, 96 registers a thread
 constexpr int kRingThreads = (kRingWarps + 1) * 32;
 constexpr int kMaxStages = 4;
 constexpr int kLongList = 16;  // tiles a block
@@ -696,7 +699,7 @@ __device__ __forceinline__ Arrays arrays_of(const AdamwTensorDev& t, float lr, u
 
 // One warp: tiles from the list to the ring, and their scales back.  Stage s
 // gets its i-th tile when the warps have emptied it of the one before.  What
-// is issued here is done in few, wide steps: among 15 busy warps an
+// is issued here is done in few, wide steps: among 19 busy warps an
 // instruction of this one takes a dozen cycles, and a tile has under 3000.
 __device__ __forceinline__ void fetch_tiles(const AdamwTable& table, Ring& ring, unsigned char* stages, int n_stages,
                                             int stride, float lr, unsigned base, AdamwHeader* hdr) {

@@ -644,3 +644,78 @@ def test_binding_refuses(torch, bd):
     assert bd.load().shampoo_adamw_step(opt._ctx, 0, 1e-3, None, None, ws.data_ptr(), ws.numel(),
                                         None) == bd.SHAMPOO_EINVAL  # another workspace
     assert opt.steps_taken() == 0 and not bool(p.any())
+
+
+# ---------------------------------------------------------------- bits
+
+@pytest.mark.parametrize("bits", [32, 8])
+def test_moments_are_those_of_fp32_rounded_operation_by_operation(torch, bd, bits):
+    # the moments' products and sums are rounded one by one, and 8-bit roots correctly: numpy's fp32 has the same
+    # bits, and with them the same codes
+    f = np.float32
+    shapes = [(40000,), (5001,)]
+    opt, guard, gen = make(torch, bd, shapes, bits, torch.float32, torch.float32, None, 0)
+    b1, b2 = f(opt.hp.beta1), f(opt.hp.beta2)
+    for t in range(1, 6):
+        for g in opt.grads:
+            g.copy_(spread(torch, gen, g.numel(), 1e-2).view(g.shape))
+        before = snapshot(opt)
+        opt.step(1e-3)
+        for i, (_, g, m0, v0) in enumerate(before):
+            g, m0, v0 = g.astype(f), m0.astype(f), v0.astype(f)
+            m = m0 * b1 + g * (f(1) - b1)
+            v = v0 * b2 + (g * (f(1) - b2)) * g
+            if bits == 32:
+                assert np.array_equal(opt.m[i].cpu().numpy(), m) and np.array_equal(opt.v[i].cpu().numpy(), v)
+                continue
+            dm, dv, _ = oa.draws(opt.hp.seed, t, i, np.arange(len(m)))
+            for x, code, scale, fmt, u in ((m, opt.m, opt.m_scale, oa.M_FORMAT, dm),
+                                           (np.sqrt(v), opt.v, opt.v_scale, oa.V_FORMAT, dv)):
+                e = oa.block_exponents(x, fmt)
+                assert np.array_equal(scale[i].cpu().numpy().astype(int) - 127, e)
+                assert np.array_equal(oa.decode(code[i].cpu().numpy(), e + 127, fmt), oa.held(x, fmt, e, u))
+    guard.check()
+
+
+def test_long_lists_are_dealt_out_completely(torch, bd):
+    # over 16 tiles of 4096 for each block, so that tiles come from the counter, in tensors of all sizes: whole tiles,
+    # short ends, other alignments, both widths; every element is stepped once, as in a list of its own
+    gen = torch.Generator("cuda").manual_seed(4)
+    sizes = [4096 * 700, 4096 * 300 + 17, 5, 4096, 4095, 4096 * 1500, 100001, 4096 * 64] + [4096 * 3 + 1] * 40
+    P, G, M, V, S = [], [], [], [], []
+    bits = [8 if i % 3 else 32 for i in range(len(sizes))]
+    for i, n in enumerate(sizes):
+        at = 1 if i % 5 == 4 else 0
+        code = torch.uint8 if bits[i] == 8 else torch.float32
+        P.append(torch.ones(n + at, device="cuda")[at:])
+        G.append(torch.randn(n + at, generator=gen, device="cuda")[at:])
+        M.append(torch.zeros(n + at, dtype=code, device="cuda")[at:])
+        V.append(torch.zeros(n + at, dtype=code, device="cuda")[at:])
+    start = [p.clone() for p in P]
+    opt = bd.AdamW(P, G, state_bits=bits, m=M, v=V, weight_decay=0.0)
+    for _ in range(2):
+        opt.step(1e-2)
+    m, v = opt.read_moments()
+    assert opt.status() == (0, 0) and opt.steps_taken() == 2
+    b1, b2 = opt.hp.beta1, opt.hp.beta2
+    for i in range(len(sizes)):
+        # Two steps of the same gradient move a parameter by 2 lr g / (|g| + eps'), eps' at most 1e-8: up to 1e-8 / |g|
+        # short of 2 lr, and 1e-4 covers the roundings beside a parameter of 1.  8-bit moments are off by a code's
+        # width in between: 1/8 of m (weight 0.9 * 0.1 of 0.19) and 1/16 of r (half of v), together under 0.1 of the
+        # second update; and for small |g| by the formats' absolute steps in a block whose largest |g| is under 6:
+        # 0.9 * 2^-9 * 2.7e-3 of m's 0.19 |g| and 1.2e-5 / 16 of r's 0.045 |g|, together under 5e-5 / |g| of the
+        # second update, 3e-5 / |g| of both.
+        moved = (start[i] - P[i]).double() / (2 * 0.01) * torch.sign(G[i].double())
+        tol = (1e-4 if bits[i] == 32 else 0.1) + (1.1e-8 if bits[i] == 32 else 3e-5) / G[i].double().abs()
+        assert bool(((moved - 1).abs() <= tol).all()), i
+        if bits[i] == 32:
+            g = G[i].double()
+            assert bool(((opt.views(v)[i].double() / (g * g * (1 - b2 * b2)) - 1).abs() < 1e-5).all())
+
+
+def test_counter_goes_on_from_a_late_step(torch, bd):
+    p, g = torch.ones(1, device="cuda"), torch.ones(1, device="cuda")
+    opt = bd.AdamW([p], [g], steps_taken=10 ** 6)
+    for _ in range(5):
+        opt.step(0.0)
+    assert opt.steps_taken() == 10 ** 6 + 5
