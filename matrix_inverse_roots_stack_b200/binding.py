@@ -581,7 +581,7 @@ class AdamW(_TensorList):
         if hasattr(lr, "data_ptr"):
             lr, lr_at, held = 0.0, self._scalar(lr, "lr"), lr
         else:
-            held = None
+            lr, held = float(lr), None
         if coef is not None:
             coef_at = self._scalar(coef, "coef")
         self._run("shampoo_adamw_step", self._ctx, step, lr, lr_at, coef_at, self._ws_at, self._ws_bytes,

@@ -273,15 +273,18 @@ static_assert(kDescWords == 11, "written as 8-byte words, one by each lane");
 // A tile in shared memory: parameters, gradients, moments and, in 8 bits,
 // scales, one behind the other.
 __host__ __device__ constexpr int type_bytes(int dtype) { return dtype == SHAMPOO_DTYPE_F32 ? 4 : 2; }
+__host__ __device__ constexpr int bulk_bytes(bool eight, int pt, int gt) {
+  return kTile * (type_bytes(pt) + type_bytes(gt) + (eight ? 2 : 8));
+}
 __host__ __device__ constexpr int staged_bytes(bool eight, int pt, int gt) {
-  return kTile * (type_bytes(pt) + type_bytes(gt) + (eight ? 2 : 8)) + (eight ? 2 * kTileBlocks : 0);
+  return bulk_bytes(eight, pt, gt) + (eight ? 2 * kTileBlocks : 0);
 }
 template <bool kEight>
 struct StagedAt {
   int grad, m, v, m_scale, v_scale;  // offsets; the parameters are at 0
   __device__ __forceinline__ StagedAt(int pt, int gt)
       : grad(kTile * type_bytes(pt)), m(grad + kTile * type_bytes(gt)), v(m + kTile * (kEight ? 1 : 4)),
-        m_scale(v + kTile), v_scale(m_scale + kTileBlocks) {}
+        m_scale(v + kTile), v_scale(m_scale + kTileBlocks) {}  // the scales: 8 bits only
 };
 
 __device__ __forceinline__ void load8_shared(const unsigned char* base, int i, int dtype, Raw8& r) {
@@ -455,7 +458,7 @@ __device__ __forceinline__ bool step_block(const TileDesc& t, int pt, int gt, in
   if (pt == SHAMPOO_DTYPE_F32) {
     char* copy = t.copy ? t.copy + 2 * at : nullptr;
     if (vec) {
-      store8(param, lane, SHAMPOO_DTYPE_F32, y);
+      store8<kAccess == kStaged>(param, lane, SHAMPOO_DTYPE_F32, y);
       if (copy) store8(copy, lane, ct, y);
     } else {
 #pragma unroll
@@ -531,8 +534,13 @@ __device__ __forceinline__ bool step_block(const TileDesc& t, int pt, int gt, in
       rm.w[2 * j] = __float_as_uint(low(m[j])), rm.w[2 * j + 1] = __float_as_uint(high(m[j]));
       rv.w[2 * j] = __float_as_uint(low(v[j])), rv.w[2 * j + 1] = __float_as_uint(high(v[j]));
     }
-    store32B(reinterpret_cast<float*>(cm) + 8 * lane, rm.w);
-    store32B(reinterpret_cast<float*>(cv) + 8 * lane, rv.w);
+    if (kAccess == kStaged) {
+      store32B_wide(reinterpret_cast<float*>(cm) + 8 * lane, rm.w);
+      store32B_wide(reinterpret_cast<float*>(cv) + 8 * lane, rv.w);
+    } else {
+      store32B(reinterpret_cast<float*>(cm) + 8 * lane, rm.w);
+      store32B(reinterpret_cast<float*>(cv) + 8 * lane, rv.w);
+    }
   } else {
 #pragma unroll
     for (int j = 0; j < 8; ++j)
@@ -620,6 +628,7 @@ __device__ __noinline__ bool step_direct(const TileDesc& t, int at, const AdamwA
 constexpr int kRingWarps = 19;  // and the fetching one: 5 to a scheduler, 96 registers a thread
 constexpr int kRingThreads = (kRingWarps + 1) * 32;
 constexpr int kMaxStages = 4;
+constexpr int kScaleLanes = 2 * kTileBlocks / 4;  // lanes of the fetching warp that fetch scales
 constexpr int kLongList = 16;  // tiles a block
 constexpr int kDeal = 4;       // tiles of one share
 constexpr int kSmemLimit = 226 * 1024;  // of an SM's 227 KB; a little is static
@@ -668,7 +677,7 @@ struct Deal {
 struct Arrays {
   char* at;            // lane's array
   unsigned rate;       // its bytes for 256 elements
-  unsigned to, bytes;  // where a tile of it goes in a stage, and its size; 0: not copied
+  unsigned to, bytes;  // where a tile of it goes in a stage, and its size; 0: not copied in bulk
   long long n;
   int first_tile, flags;
   unsigned tensor_key, key;
@@ -693,7 +702,7 @@ __device__ __forceinline__ Arrays arrays_of(const AdamwTensorDev& t, float lr, u
   a.rate = lane == 0 ? p : lane == 1 ? g : lane < 4 ? m : lane < 6 ? 1u : 512u;
   const unsigned before = (lane > 0 ? p : 0u) + (lane > 1 ? g : 0u) + (lane > 2 ? m : 0u) + (lane > 3 ? m : 0u) + (lane > 4 ? 1u : 0u);
   a.to = before * (kTile / 256);
-  a.bytes = lane < (eight ? 6 : 4) ? a.rate * (kTile / 256) : 0u;
+  a.bytes = lane < 4 ? a.rate * (kTile / 256) : 0u;
   return a;
 }
 
@@ -734,7 +743,7 @@ __device__ __forceinline__ void fetch_tiles(const AdamwTable& table, Ring& ring,
         a.high = high;
         a.key = key_word(a.tensor_key, static_cast<unsigned>(high));
       }
-      staged = (a.flags & kFlagBulk) && left == kTile;
+      staged = (a.flags & kFlagWide) && left == kTile;
       from = a.at ? a.at + ((static_cast<unsigned long long>(e0) * a.rate) >> 8) : nullptr;
       const unsigned lo = lane == 7 ? left : lane == 8 ? a.key : lane == 9 ? __float_as_uint(a.neg_lr) : staged;
       const unsigned hi = lane == 7 ? a.flags : lane == 8 ? static_cast<unsigned>(e0) : lane == 9 ? __float_as_uint(a.decay) : 0u;
@@ -752,12 +761,21 @@ __device__ __forceinline__ void fetch_tiles(const AdamwTable& table, Ring& ring,
     if (lane < kDescWords) reinterpret_cast<unsigned long long*>(&ring.tile[s])[lane] = word;
     __syncwarp();
     uint64_t* bar = &ring.full[s];
+    unsigned char* to = stages + s * stride;
     if (lane == 0) {
-      if (staged) mbar_arrive_expect_tx(bar, staged_bytes(a.flags & kFlagEight, (a.flags >> kParamShift) & 15, (a.flags >> kGradShift) & 15));
+      if (staged) mbar_arrive_expect_tx(bar, bulk_bytes(a.flags & kFlagEight, (a.flags >> kParamShift) & 15, (a.flags >> kGradShift) & 15));
       else mbar_arrive(bar);
     }
     __syncwarp();
-    if (staged && a.bytes) bulk_load(stages + s * stride + a.to, from, a.bytes, bar);
+    if (staged && a.bytes) bulk_load(to + a.to, from, a.bytes, bar);
+    // the scales, 16 bytes of m's and 16 of v's, four to a lane: a scale array need not be aligned for bulk copies
+    const unsigned long long at_m = __shfl_sync(0xffffffffu, word, 4), at_v = __shfl_sync(0xffffffffu, word, 5);
+    const unsigned at_scales = __shfl_sync(0xffffffffu, a.to, 4);
+    if (lane < kScaleLanes) {
+      if (staged && (a.flags & kFlagEight))
+        copy4_async(to + at_scales + 4 * lane, reinterpret_cast<const char*>(lane < 4 ? at_m : at_v) + 4 * (lane & 3));
+      arrive_behind_copies(bar);
+    }
     if (scale) write_scale(scale, most);
     __syncwarp();
     if (!dealt || deal.left-- > 0) {
@@ -802,7 +820,7 @@ __device__ __forceinline__ void adamw_step(const AdamwTable& table, AdamwHeader*
   const bool skip = not_finite(k.coef);  // non-finite gradients: the step is not taken
   if (threadIdx.x == 0) {
     for (int s = 0; s < n_stages; ++s) {
-      mbar_init(&ring.full[s], 1);
+      mbar_init(&ring.full[s], 1 + kScaleLanes);
       mbar_init(&ring.empty[s], kRingWarps);
     }
     ring.abort = 0;

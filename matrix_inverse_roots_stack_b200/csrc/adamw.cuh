@@ -26,11 +26,11 @@ static_assert(sizeof(AdamwTensorDev) == 96, "six 16-byte words");
 
 constexpr int kParamShift = 0, kGradShift = 4, kCopyShift = 8;  // element types in AdamwTensorDev::flags
 constexpr int kFlagEight = 1 << 12;                             // 8-bit moments
-constexpr int kFlagVec = 1 << 13;                               // every pointer allows eight-element accesses
-constexpr int kFlagBulk = 1 << 14;                              // and bulk copies: 16-byte aligned
+constexpr int kFlagVec = 1 << 13;                               // every array but the scales is on a 16-byte boundary
+constexpr int kFlagWide = 1 << 14;  // and written fp32 on a 32-byte one, scales on a 4-byte one: tiles can be staged
 
-// Elements that the step takes at a time: 16 blocks, so that their scales are
-// one 16-byte copy.
+// Elements that the step takes at a time: 16 blocks, a scale of m and of v for
+// each lane of a warp.
 constexpr int kTileBlocks = 16;
 constexpr int kTile = kTileBlocks * kQBlock;
 

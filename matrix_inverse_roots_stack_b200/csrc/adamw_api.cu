@@ -48,18 +48,22 @@ bool tensor_ok(const shampoo_adamw_tensor& q) {
          dash::aligned_to(q.m, ms) && dash::aligned_to(q.v, ms);
 }
 
-// Whether every pointer lets a lane take eight elements in one access.
+// Whether every array but the scales lies on a 16-byte boundary, so that bulk
+// copies and accesses of eight elements reach it.
 bool vector_ok(const shampoo_adamw_tensor& q) {
-  const size_t ms = q.state_bits == 32 ? 32 : 8;
-  return dash::aligned_to(q.param, 8 * dash::dtype_bytes(q.param_dtype)) &&
-         dash::aligned_to(q.grad, 8 * dash::dtype_bytes(q.grad_dtype)) && dash::aligned_to(q.copy, 16) &&
-         dash::aligned_to(q.m, ms) && dash::aligned_to(q.v, ms);
+  bool ok = true;
+  for (const void* p : {static_cast<const void*>(q.param), q.grad, static_cast<const void*>(q.copy),
+                        static_cast<const void*>(q.m), static_cast<const void*>(q.v)})
+    ok = ok && dash::aligned_to(p, 16);
+  return ok;
 }
 
-// Whether bulk copies (16-byte aligned) may read it too.
-bool bulk_ok(const shampoo_adamw_tensor& q) {
-  return vector_ok(q) && dash::aligned_to(q.m, 16) && dash::aligned_to(q.v, 16) &&
-         (q.state_bits == 32 || (dash::aligned_to(q.m_scale, 16) && dash::aligned_to(q.v_scale, 16)));
+// And whether eight fp32 elements can be written in one access, and scales
+// fetched four at a time.
+bool wide_ok(const shampoo_adamw_tensor& q) {
+  if (!vector_ok(q) || (q.param_dtype == SHAMPOO_DTYPE_F32 && !dash::aligned_to(q.param, 32))) return false;
+  return q.state_bits == 32 ? dash::aligned_to(q.m, 32) && dash::aligned_to(q.v, 32)
+                            : dash::aligned_to(q.m_scale, 4) && dash::aligned_to(q.v_scale, 4);
 }
 
 void add_tensor(shampoo_adamw* c, const shampoo_adamw_tensor& q, int index) {
@@ -77,7 +81,7 @@ void add_tensor(shampoo_adamw* c, const shampoo_adamw_tensor& q, int index) {
   r.first_tile = static_cast<int>(c->tiles);
   r.flags = (q.param_dtype << dash::kParamShift) | (q.grad_dtype << dash::kGradShift) |
             ((q.copy ? q.copy_dtype : 0) << dash::kCopyShift) | (eight ? dash::kFlagEight : 0) |
-            (vector_ok(q) ? dash::kFlagVec : 0) | (bulk_ok(q) ? dash::kFlagBulk : 0);
+            (vector_ok(q) ? dash::kFlagVec : 0) | (wide_ok(q) ? dash::kFlagWide : 0);
   r.index = index;
   r.lr_scale = q.lr_scale;
   r.decay = q.weight_decay;
@@ -108,6 +112,9 @@ int check_bound(const shampoo_adamw* c, const void* ws, size_t ws_bytes) {
   if (!ws || ws_bytes < c->total) return SHAMPOO_EWORKSPACE;
   return ws == c->bound_ws ? SHAMPOO_OK : SHAMPOO_EINVAL;
 }
+
+// Flat moments; a list without elements has none.
+bool flat_ok(const shampoo_adamw* c, const void* p) { return c->blocks == 0 || (p && dash::aligned_to(p, 16)); }
 
 AdamwTable table(const shampoo_adamw* c, const void* ws) {
   const char* w = static_cast<const char*>(ws);
@@ -238,7 +245,7 @@ int shampoo_adamw_load_moments(shampoo_adamw* c, const float* m, const float* v,
                                void* stream) {
   const int rc = check_bound(c, ws, ws_bytes);
   if (rc) return rc;
-  if (!m || !v || !dash::aligned_to(m, 32) || !dash::aligned_to(v, 32)) return SHAMPOO_EINVAL;
+  if (!flat_ok(c, m) || !flat_ok(c, v)) return SHAMPOO_EINVAL;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (cudaMemsetAsync(ws, 0, sizeof(unsigned), st) != cudaSuccess) return SHAMPOO_ECUDA;
   if (c->blocks == 0) return SHAMPOO_OK;
@@ -250,8 +257,7 @@ int shampoo_adamw_read_moments(shampoo_adamw* c, void* m, void* v, int dtype, vo
                                void* stream) {
   const int rc = check_bound(c, ws, ws_bytes);
   if (rc) return rc;
-  if (!m || !v || (dtype != SHAMPOO_DTYPE_F32 && dtype != SHAMPOO_DTYPE_BF16) || !dash::aligned_to(m, 32) ||
-      !dash::aligned_to(v, 32))
+  if ((dtype != SHAMPOO_DTYPE_F32 && dtype != SHAMPOO_DTYPE_BF16) || !flat_ok(c, m) || !flat_ok(c, v))
     return SHAMPOO_EINVAL;
   if (c->blocks == 0) return SHAMPOO_OK;
   dash::launch_read_moments(table(c, ws), m, v, dtype, static_cast<cudaStream_t>(stream));

@@ -18,7 +18,7 @@ namespace {
 struct GradChunk {
   void* grad;
   int count;   // elements, at most the list's chunk size
-  int flags;   // element type, and kVec when the start is aligned to eight elements
+  int flags;   // element type, and kVec when the start is on a 16-byte boundary
 };
 constexpr int kVec = 16;
 constexpr int kTypeMask = 15;
@@ -208,7 +208,7 @@ int shampoo_grads_init(shampoo_grads** out, const shampoo_grad* grads, int n_gra
       }
       const size_t size = dash::dtype_bytes(g.dtype);
       dash::add_range(ranges, g.grad, size * static_cast<size_t>(g.n), true);
-      const int flags = g.dtype | (dash::aligned_to(g.grad, 8 * size) ? dash::kVec : 0);
+      const int flags = g.dtype | (dash::aligned_to(g.grad, 16) ? dash::kVec : 0);
       for (int64_t at = 0; at < g.n; at += dash::kChunk)
         c->chunks.push_back({static_cast<char*>(g.grad) + size * static_cast<size_t>(at),
                              static_cast<int>(std::min<int64_t>(dash::kChunk, g.n - at)), flags});

@@ -57,18 +57,33 @@ struct Raw8 {
   unsigned w[8];
 };
 
-// 256-bit accesses (sm_100): a lane's eight fp32 elements in one instruction,
-// so that a warp covers 1 KB without a strided second access.
+// A lane's eight fp32 elements, from a 16-byte boundary.  On a 32-byte one
+// they are one 256-bit access (sm_100), and a warp covers 1 KB without a
+// strided second access.
+__device__ __forceinline__ bool half_sector(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 16u) != 0; }
 __device__ __forceinline__ void load32B(const void* p, unsigned* w) {
+  if (half_sector(p)) {
+    const uint4 a = static_cast<const uint4*>(p)[0], b = static_cast<const uint4*>(p)[1];
+    w[0] = a.x, w[1] = a.y, w[2] = a.z, w[3] = a.w, w[4] = b.x, w[5] = b.y, w[6] = b.z, w[7] = b.w;
+    return;
+  }
   asm volatile("ld.global.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
                : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7])
                : "l"(p)
                : "memory");
 }
-__device__ __forceinline__ void store32B(void* p, const unsigned* w) {
+__device__ __forceinline__ void store32B_wide(void* p, const unsigned* w) {  // from a 32-byte boundary
   asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]),
                "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
                : "memory");
+}
+__device__ __forceinline__ void store32B(void* p, const unsigned* w) {
+  if (half_sector(p)) {
+    static_cast<uint4*>(p)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+    static_cast<uint4*>(p)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+  } else {
+    store32B_wide(p, w);
+  }
 }
 
 __device__ __forceinline__ float widen(unsigned short b, int dtype) {
@@ -88,8 +103,8 @@ __device__ __forceinline__ unsigned narrow2(float lo, float hi, int dtype) {
   return *reinterpret_cast<const unsigned*>(&h);
 }
 
-// Vector path: elements 8 i .. 8 i + 7 of a buffer whose start is aligned to
-// eight elements.
+// Vector path: elements 8 i .. 8 i + 7 of a buffer that starts on a 16-byte
+// boundary.
 __device__ __forceinline__ void load8(const void* base, int i, int dtype, Raw8& r) {
   if (dtype == SHAMPOO_DTYPE_F32) {
     load32B(static_cast<const float*>(base) + 8ll * i, r.w);
@@ -117,12 +132,14 @@ __device__ __forceinline__ void widen8(const Raw8& r, int dtype, float* x) {
     }
   }
 }
+template <bool kWide = false>  // fp32 from a 32-byte boundary
 __device__ __forceinline__ void store8(void* base, int i, int dtype, const float* x) {
   if (dtype == SHAMPOO_DTYPE_F32) {
     unsigned w[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) w[j] = __float_as_uint(x[j]);
-    store32B(static_cast<float*>(base) + 8ll * i, w);
+    if (kWide) store32B_wide(static_cast<float*>(base) + 8ll * i, w);
+    else store32B(static_cast<float*>(base) + 8ll * i, w);
   } else {
     *(static_cast<uint4*>(base) + i) = make_uint4(narrow2(x[0], x[1], dtype), narrow2(x[2], x[3], dtype),
                                                   narrow2(x[4], x[5], dtype), narrow2(x[6], x[7], dtype));

@@ -7,6 +7,8 @@ result.  8-bit codes and bf16 parameters are compared with the neighbours that
 the oracle's value, moved by its tolerance either way, is rounded to.
 """
 
+import math
+
 import numpy as np
 import pytest
 
@@ -161,10 +163,10 @@ def check_step(torch, opt, before, t, lr, coef=1.0, decay=0.1, lr_scale=1.0):
 
 
 @pytest.mark.parametrize("bits", [32, 8])
-@pytest.mark.parametrize("offset", [0, 1])
+@pytest.mark.parametrize("offset", [0, 1, 4, 8, 16])
 @pytest.mark.parametrize("param,grad,copy", [("float32", "float32", None), ("float32", "bfloat16", "bfloat16"),
                                              ("float32", "float16", "float16"), ("bfloat16", "bfloat16", None),
-                                             ("bfloat16", "float32", None)])
+                                             ("bfloat16", "float32", None), ("bfloat16", "float16", None)])
 def test_steps_match_the_oracle(torch, bd, bits, offset, param, grad, copy):
     ty = lambda s: getattr(torch, s) if s else None
     hp = bd.make_adamw_hparams(seed=77 + (5 << 32))
@@ -215,7 +217,7 @@ def test_no_gradient_leaves_zero_moments(torch, bd):
 @pytest.mark.parametrize("bits", [32, 8])
 def test_scalar_and_vector_accesses_give_the_same_bits(torch, bd, bits):
     out = []
-    for offset in (0, 1):
+    for offset in (0, 1, 4, 16):
         opt, guard, gen = make(torch, bd, SIZES + [(9000,)], bits, torch.bfloat16, torch.bfloat16, None, offset)
         for _ in range(3):
             for g in opt.grads:
@@ -223,7 +225,7 @@ def test_scalar_and_vector_accesses_give_the_same_bits(torch, bd, bits):
             opt.step(1e-2)
         out.append([t.clone() for t in opt.params + opt.m + opt.v + opt.m_scale + opt.v_scale if t is not None])
         guard.check()
-    assert all(torch.equal(a, b) for a, b in zip(*out))
+    assert all(torch.equal(a, b) for other in out[1:] for a, b in zip(out[0], other))
 
 
 def test_list_of_both_moment_widths_and_settings_for_each(torch, bd):
@@ -449,7 +451,7 @@ def test_bf16_parameters_collect_small_updates(torch, bd):
 
 # ---------------------------------------------------------------- moments in and out
 
-@pytest.mark.parametrize("offset", [0, 1])
+@pytest.mark.parametrize("offset", [0, 1, 4, 16])
 @pytest.mark.parametrize("dtype", ["float32", "bfloat16"])
 def test_moments_in_and_out(torch, bd, offset, dtype):
     opt, guard, gen = make(torch, bd, SIZES, 8, torch.float32, torch.float32, None, offset)
@@ -719,3 +721,41 @@ def test_counter_goes_on_from_a_late_step(torch, bd):
     for _ in range(5):
         opt.step(0.0)
     assert opt.steps_taken() == 10 ** 6 + 5
+
+
+def test_list_without_elements(torch, bd):
+    e = lambda: torch.zeros(0, device="cuda")
+    for bits in (32, 8):
+        opt = bd.AdamW([e(), e()], [e(), e()], state_bits=bits)
+        assert opt.moment_elems == 0
+        for _ in range(3):
+            opt.step(1e-3)
+        opt.load_moments(e(), e())
+        assert [t.numel() for t in opt.read_moments()] == [0, 0]
+        assert opt.status() == (0, 0) and opt.steps_taken() == 3
+
+
+def test_thousands_of_small_tensors(torch, bd):
+    # the search for a tile's tensor goes 32 ways over several levels
+    rng = np.random.default_rng(6)
+    sizes = rng.integers(0, 600, 5000).tolist()
+    total = sum(sizes)
+    gen = torch.Generator("cuda").manual_seed(8)
+    flat = {k: torch.randn(total, generator=gen, device="cuda") for k in "pg"}
+    start = flat["p"].clone()
+    ends = np.cumsum([0] + sizes)
+    cut = lambda x: [x[a:b] for a, b in zip(ends[:-1], ends[1:])]
+    opt = bd.AdamW(cut(flat["p"]), cut(flat["g"]), state_bits=[8 if i % 2 else 32 for i in range(5000)])
+    clip = bd.GradClip(cut(flat["g"]))
+    opt.step(0.5)
+    # eps' beside |g|, and a dozen roundings of the update and one of the parameter
+    g = flat["g"].double()
+    want = start.double() - 0.5 * g / (g.abs() + float(np.float32(1e-8)))
+    assert bool(((flat["p"].double() - want).abs() <= 0.5 * 16 * H + H * want.abs() * 1.01 + 1e-15).all())
+    m, _ = opt.read_moments()
+    for i in (0, 1, 31, 32, 33, 1023, 1024, 1025, 4998, 4999):
+        if sizes[i]:
+            x = f64(opt.views(m)[i]) / (0.1 * f64(opt.grads[i]))
+            assert np.all(np.abs(x[np.abs(f64(opt.grads[i])) > 0.05] - 1) < (1e-6 if i % 2 == 0 else 0.13))
+    n = math.sqrt(float((g * g).sum()))
+    assert abs(clip.norm()[0].item() - n) <= 1.01 * H * n

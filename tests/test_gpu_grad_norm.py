@@ -48,7 +48,7 @@ SIZES = [[1], [0, 7, 0], [8191, 8192, 8193], [1, 255, 256, 257, 100003], [3_000_
 
 @pytest.mark.parametrize("sizes", SIZES)
 @pytest.mark.parametrize("dtype", ["float32", "bfloat16", "float16"])
-@pytest.mark.parametrize("offset", [0, 1])
+@pytest.mark.parametrize("offset", [0, 1, 4, 8])
 def test_norm_and_clip(torch, bd, sizes, dtype, offset):
     dtype = getattr(torch, dtype)
     grads = grads_of(torch, sizes, dtype, offset)
