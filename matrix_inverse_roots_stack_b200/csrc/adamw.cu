@@ -985,54 +985,80 @@ __global__ void __launch_bounds__(kListThreads) load_moments_kernel(const AdamwT
 }
 
 // The list's moments as flat fp32 or bf16 values; what lies behind a tensor's
-// end, up to the next multiple of kQBlock, is written as zeros.
-__global__ void __launch_bounds__(kListThreads) read_moments_kernel(const AdamwTable table, void* m_out, void* v_out,
-                                                                    int dtype) {
-  const int lane = threadIdx.x & 31;
-  const size_t size = dtype == SHAMPOO_DTYPE_F32 ? 4 : 2;
-  const AdamwTensorDev& t = table.tensors[first_tensor(table.first_tile, table.n_tensors, static_cast<int>(blockIdx.x))];
-  const long long tile0 = static_cast<long long>(static_cast<int>(blockIdx.x) - t.first_tile) * kTile;
+// end, up to the next multiple of kQBlock, is written as zeros.  A warp has
+// four blocks of the tile, and asks for all of their codes and scales before
+// it uses any: 6 or 10 bytes an element are little to hide HBM's latency with.
+constexpr int kReadBlocks = 4;
+constexpr int kReadThreads = kTileBlocks / kReadBlocks * 32;
+
+__device__ __forceinline__ void write_moments(const AdamwTensorDev& t, long long e0, f32x2* m, f32x2* v, bool squared,
+                                              void* m_out, void* v_out, int dtype) {
+  const int lane = threadIdx.x & 31, left = static_cast<int>(min(static_cast<long long>(kQBlock), t.n - e0));
+  const size_t at = (dtype == SHAMPOO_DTYPE_F32 ? 4 : 2) * static_cast<size_t>(static_cast<long long>(t.first) * kQBlock + e0);
+  float x[8], y[8];
 #pragma unroll
-  for (int w = 0; w < kTileBlocks / kListWarps; ++w) {
-    const long long e0 = tile0 + ((threadIdx.x >> 5) + w * kListWarps) * kQBlock;
+  for (int j = 0; j < 8; ++j) {
+    const bool in = 8 * lane + j < left;
+    if (!squared && !(j & 1)) v[j / 2] = mul2(v[j / 2], v[j / 2]);
+    x[j] = !in ? 0.0f : j & 1 ? high(m[j / 2]) : low(m[j / 2]);
+    y[j] = !in ? 0.0f : j & 1 ? high(v[j / 2]) : low(v[j / 2]);
+  }
+  store8(static_cast<char*>(m_out) + at, lane, dtype, x);
+  store8(static_cast<char*>(v_out) + at, lane, dtype, y);
+}
+
+__global__ void __launch_bounds__(kReadThreads) read_moments_kernel(const AdamwTable table, void* m_out, void* v_out,
+                                                                    int dtype) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const AdamwTensorDev& t = table.tensors[first_tensor(table.first_tile, table.n_tensors, static_cast<int>(blockIdx.x))];
+  const long long first = static_cast<long long>(static_cast<int>(blockIdx.x) - t.first_tile) * kTile + warp * (kReadBlocks * kQBlock);
+  f32x2 m[4], v[4];
+  if ((t.flags & kFlagEight) && (t.flags & kFlagVec) && first + kReadBlocks * kQBlock <= t.n) {
+    uint2 qm[kReadBlocks], qv[kReadBlocks];
+    int ms[kReadBlocks], vs[kReadBlocks];
+#pragma unroll
+    for (int w = 0; w < kReadBlocks; ++w) {
+      const long long e0 = first + w * kQBlock;
+      qm[w] = *(reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(t.m) + e0) + lane);
+      qv[w] = *(reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(t.v) + e0) + lane);
+      ms[w] = t.m_scale[e0 >> 8];
+      vs[w] = t.v_scale[e0 >> 8];
+    }
+#pragma unroll
+    for (int w = 0; w < kReadBlocks; ++w) {
+      const f32x2 mf = both(m8_factor(ms[w])), vf = both(v8_factor(vs[w]));
+      m8_values4(qm[w].x, mf, m);
+      m8_values4(qm[w].y, mf, m + 2);
+      v8_values4(qv[w].x, vf, v);
+      v8_values4(qv[w].y, vf, v + 2);
+      write_moments(t, first + w * kQBlock, m, v, false, m_out, v_out, dtype);
+    }
+    return;
+  }
+  for (int w = 0; w < kReadBlocks; ++w) {
+    const long long e0 = first + w * kQBlock;
     if (e0 >= t.n) break;
-    const long long flat = static_cast<long long>(t.first) * kQBlock + e0;
-    const int left = static_cast<int>(min(static_cast<long long>(kQBlock), t.n - e0));
-    const bool vec = (t.flags & kFlagVec) && left == kQBlock;
-    const int i0 = 8 * lane;
-    char* om = static_cast<char*>(m_out) + size * flat;
-    char* ov = static_cast<char*>(v_out) + size * flat;
-    f32x2 m[4], v[4];
+    const int left = static_cast<int>(min(static_cast<long long>(kQBlock), t.n - e0)), i0 = 8 * lane;
     if (t.flags & kFlagEight) {
       const uint8_t* cm = static_cast<const uint8_t*>(t.m) + e0;
       const uint8_t* cv = static_cast<const uint8_t*>(t.v) + e0;
-      uint2 qm = make_uint2(0, 0), qv = make_uint2(0, 0);
-      if (vec) {
-        qm = *(reinterpret_cast<const uint2*>(cm) + lane);
-        qv = *(reinterpret_cast<const uint2*>(cv) + lane);
-      } else {
-        unsigned am[2] = {0, 0}, av[2] = {0, 0};
+      unsigned am[2] = {0, 0}, av[2] = {0, 0};
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-          if (i0 + j < left) {
-            am[j >> 2] |= static_cast<unsigned>(cm[i0 + j]) << (8 * (j & 3));
-            av[j >> 2] |= static_cast<unsigned>(cv[i0 + j]) << (8 * (j & 3));
-          }
-        qm = make_uint2(am[0], am[1]);
-        qv = make_uint2(av[0], av[1]);
-      }
+      for (int j = 0; j < 8; ++j)
+        if (i0 + j < left) {
+          am[j >> 2] |= static_cast<unsigned>(cm[i0 + j]) << (8 * (j & 3));
+          av[j >> 2] |= static_cast<unsigned>(cv[i0 + j]) << (8 * (j & 3));
+        }
       const f32x2 mf = both(m8_factor(t.m_scale[e0 >> 8])), vf = both(v8_factor(t.v_scale[e0 >> 8]));
-      m8_values4(qm.x, mf, m);
-      m8_values4(qm.y, mf, m + 2);
-      v8_values4(qv.x, vf, v);
-      v8_values4(qv.y, vf, v + 2);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) v[j] = mul2(v[j], v[j]);
+      m8_values4(am[0], mf, m);
+      m8_values4(am[1], mf, m + 2);
+      v8_values4(av[0], vf, v);
+      v8_values4(av[1], vf, v + 2);
     } else {
       const float* fm = static_cast<const float*>(t.m) + e0;
       const float* fv = static_cast<const float*>(t.v) + e0;
       Raw8 rm, rv;
-      if (vec) {
+      if ((t.flags & kFlagVec) && left == kQBlock) {
         load32B(fm + i0, rm.w);
         load32B(fv + i0, rv.w);
       } else {
@@ -1048,15 +1074,7 @@ __global__ void __launch_bounds__(kListThreads) read_moments_kernel(const AdamwT
         v[j] = pack2(__uint_as_float(rv.w[2 * j]), __uint_as_float(rv.w[2 * j + 1]));
       }
     }
-    float x[8], y[8];
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const bool in = vec || i0 + j < left;
-      x[j] = !in ? 0.0f : j & 1 ? high(m[j / 2]) : low(m[j / 2]);
-      y[j] = !in ? 0.0f : j & 1 ? high(v[j / 2]) : low(v[j / 2]);
-    }
-    store8(om, lane, dtype, x);
-    store8(ov, lane, dtype, y);
+    write_moments(t, e0, m, v, !(t.flags & kFlagEight), m_out, v_out, dtype);
   }
 }
 
@@ -1101,7 +1119,7 @@ void launch_load_moments(const AdamwTable& t, AdamwHeader* hdr, const float* m, 
 }
 
 void launch_read_moments(const AdamwTable& t, void* m, void* v, int dtype, cudaStream_t st) {
-  read_moments_kernel<<<t.n_tiles, kListThreads, 0, st>>>(t, m, v, dtype);
+  read_moments_kernel<<<t.n_tiles, kReadThreads, 0, st>>>(t, m, v, dtype);
   prof_count_launch();
 }
 
