@@ -711,7 +711,7 @@ __device__ __forceinline__ Arrays arrays_of(const AdamwTensorDev& t, float lr, u
 // is issued here is done in few, wide steps: among 19 busy warps an
 // instruction of this one takes a dozen cycles, and a tile has under 3000.
 __device__ __forceinline__ void fetch_tiles(const AdamwTable& table, Ring& ring, unsigned char* stages, int n_stages,
-                                            int stride, float lr, unsigned base, AdamwHeader* hdr) {
+                                            int stride, float lr, unsigned base, bool withhold, AdamwHeader* hdr) {
   const int lane = threadIdx.x & 31, grid = gridDim.x;
   const bool dealt = table.n_tiles / kLongList >= grid;
   Deal deal(table.n_tiles, grid);
@@ -767,7 +767,7 @@ __device__ __forceinline__ void fetch_tiles(const AdamwTable& table, Ring& ring,
       else mbar_arrive(bar);
     }
     __syncwarp();
-    if (staged && a.bytes) bulk_load(to + a.to, from, a.bytes, bar);
+    if (staged && a.bytes && !withhold) bulk_load(to + a.to, from, a.bytes, bar);
     // the scales, 16 bytes of m's and 16 of v's, four to a lane: a scale array need not be aligned for bulk copies
     const unsigned long long at_m = __shfl_sync(0xffffffffu, word, 4), at_v = __shfl_sync(0xffffffffu, word, 5);
     const unsigned at_scales = __shfl_sync(0xffffffffu, a.to, 4);
@@ -800,9 +800,9 @@ __device__ __forceinline__ void fetch_tiles(const AdamwTable& table, Ring& ring,
     give_up(ring, hdr);
     // copies in flight land before the block ends: each stage's last tile, of this turn or the one before
     int never = 0;
-    for (int j = 0; j < n_stages; ++j) {
+    for (int j = 0; j < n_stages && !withhold; ++j) {
       const int turn = static_cast<int>(i) - (j < s ? 0 : 1);
-      if (turn >= 0) mbar_wait(&ring.full[j], turn & 1, &never);
+      if (turn >= 0 && !mbar_wait(&ring.full[j], turn & 1, &never)) break;
     }
   }
 }
@@ -828,7 +828,7 @@ __device__ __forceinline__ void adamw_step(const AdamwTable& table, AdamwHeader*
   }
   __syncthreads();
   if (!skip && warp == kRingWarps) {
-    fetch_tiles(table, ring, stages, n_stages, stride, k.lr, step_key(a, t), hdr);
+    fetch_tiles(table, ring, stages, n_stages, stride, k.lr, step_key(a, t), a.withhold, hdr);
   } else if (!skip) {
     // the tiles' blocks are dealt to the warps one after another; every warp waits for every tile and arrives when
     // done with it, also where it has no block, so that a stage's phases cannot run ahead of a warp

@@ -59,6 +59,7 @@ struct AdamwArgs {
   float2 one;            // 1, not known as such when the kernel is compiled
   float eps;
   unsigned seed_lo, seed_hi;
+  int withhold;          // test hook: tiles are announced and not copied, so that the waits for them run out
   int step;              // > 0: take this step number and the values below; 0: the header's next
   // m_hat / (sqrt(v_hat) + eps) = m / (d1 sqrt(v) + d0): d1 = (1 - beta1^t) / sqrt(1 - beta2^t),
   // d0 = eps (1 - beta1^t)

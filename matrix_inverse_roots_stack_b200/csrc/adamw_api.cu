@@ -5,6 +5,7 @@
 #include <new>
 
 #include "adamw.cuh"
+#include "gemm.cuh"
 #include "profile.cuh"
 
 using dash::AdamwHeader;
@@ -222,6 +223,7 @@ int shampoo_adamw_step(shampoo_adamw* c, int step, float lr, const float* lr_dev
   a.eps = c->hp.adam_eps;
   a.seed_lo = static_cast<unsigned>(c->hp.seed);
   a.seed_hi = static_cast<unsigned>(c->hp.seed >> 32);
+  a.withhold = dash::take_load_fault() ? 1 : 0;
   a.step = step;
   if (step > 0) {
     const StepConstants s = step_constants(c->hp, step);

@@ -723,6 +723,64 @@ def test_counter_goes_on_from_a_late_step(torch, bd):
     assert opt.steps_taken() == 10 ** 6 + 5
 
 
+def test_waits_for_tiles_are_bounded(torch, bd):
+    # the loads of one step are withheld: its waits run out, the launch ends and says so, and the next step is whole
+    p, g = torch.ones(4096 * 3 + 5, device="cuda"), torch.ones(4096 * 3 + 5, device="cuda")
+    opt = bd.AdamW([p], [g], state_bits=8, weight_decay=0.0)
+    assert bd.load().shampoo_debug_inject_timeout() == 0
+    opt.step(1e-2)
+    assert opt.status() == (bd.SHAMPOO_ETIMEOUT, 2)
+    for t in (p, g):
+        t.fill_(1.0)
+    for t in opt.m + opt.v + opt.m_scale + opt.v_scale:
+        t.zero_()
+    opt.step(1e-2, step=1)
+    assert opt.status() == (0, 0) and opt.steps_taken() == 1
+    assert bool(((p - 0.99).abs() <= 1e-6).all())
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+def test_betas_of_zero(torch, bd, bits):
+    hp = bd.make_adamw_hparams(beta1=0.0, beta2=0.0, seed=1)
+    opt, guard, gen = make(torch, bd, [(5000,), (3,)], bits, torch.float32, torch.float32, None, 0, hp=hp)
+    for t in range(1, 4):
+        for g in opt.grads:
+            g.copy_(torch.randn(g.shape, generator=gen))
+        before = snapshot(opt)
+        opt.step(1e-2)
+        check_step(torch, opt, before, t, 1e-2)
+    guard.check()
+
+
+def test_parameters_of_a_module_on_a_stream_of_ones_own(torch, bd):
+    # nn.Parameters with their .grad, made and stepped inside a stream context, moments in and out captured
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        net = torch.nn.Sequential(torch.nn.Linear(70, 90), torch.nn.LayerNorm(90)).cuda()
+        net(torch.randn(8, 70, device="cuda")).square().sum().backward()
+        params = list(net.parameters())
+        opt = bd.AdamW(params, [p.grad for p in params], state_bits=[8, 32, 8, 32])
+        clip = bd.GradClip([p.grad for p in params])
+        old = [p.detach().clone() for p in params]
+        opt.step(1e-2, coef=clip.norm(1.0)[1:])
+        assert opt.status() == (0, 0)
+        assert all(not torch.equal(a, p) for a, p in zip(old, params) if bool(p.grad.any()))
+        m, v = opt.read_moments()
+        copy = [t.clone() for t in opt.m + opt.v]
+        graph = torch.cuda.CUDAGraph()
+        s.synchronize()
+        with torch.cuda.graph(graph, stream=s):
+            opt.load_moments(m, v)
+            out = opt.read_moments(torch.bfloat16)
+        for t in opt.m + opt.v:
+            t.zero_()
+        graph.replay()
+        s.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(copy[1::2], (opt.m + opt.v)[1::2]))
+    assert torch.equal(out[0], m.bfloat16()) and torch.equal(out[1], v.bfloat16())
+
+
 def test_list_without_elements(torch, bd):
     e = lambda: torch.zeros(0, device="cuda")
     for bits in (32, 8):
