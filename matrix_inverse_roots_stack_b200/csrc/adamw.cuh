@@ -74,6 +74,7 @@ struct AdamwArgs {
 // their shared memory.
 struct AdamwLaunch {
   int step;
+  int direct;                // lists of up to so many tiles go without the ring
   int bits;                  // 32, 8, or 0 for both
   int stages, stride, smem;
 };

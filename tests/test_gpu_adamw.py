@@ -70,11 +70,12 @@ def spread(torch, gen, n, std):
 SIZES = [(0,), (1,), (7,), (31,), (255,), (256,), (257,), (33, 65), (2048,), (2049,), (3, 5, 700), ()]
 
 
-def make(torch, bd, sizes, bits, param, grad, copy, offset, seed=0, hp=None, decay=0.1, lr_scale=1.0):
+def make(torch, bd, sizes, bits, param, grad, copy, offsets, seed=0, hp=None, decay=0.1, lr_scale=1.0):
     gen = torch.Generator().manual_seed(seed)
     g = Guarded(torch)
     P, G, C, M, V, S = [], [], [], [], [], []
-    for shape in sizes:
+    for i, shape in enumerate(sizes):
+        offset = offsets[i % len(offsets)] if isinstance(offsets, list) else offsets
         n = int(np.prod(shape))
         P.append(g((torch.randn(n, generator=gen) * 0.02).view(shape), param, offset))
         G.append(g(torch.zeros(shape), grad, offset))
@@ -183,6 +184,26 @@ def test_steps_match_the_oracle(torch, bd, bits, offset, param, grad, copy):
 
 
 @pytest.mark.parametrize("bits", [32, 8])
+@pytest.mark.parametrize("param,grad,copy", [("float32", "float32", None), ("float32", "bfloat16", "float16"),
+                                             ("float32", "float16", "bfloat16"), ("bfloat16", "bfloat16", None),
+                                             ("bfloat16", "float32", None), ("bfloat16", "float16", None)])
+def test_steps_of_longer_lists_match_the_oracle(torch, bd, bits, param, grad, copy):
+    # more tiles than SMs: these go through the ring, whole tiles staged, others not
+    ty = lambda s: getattr(torch, s) if s else None
+    hp = bd.make_adamw_hparams(seed=78)
+    opt, guard, gen = make(torch, bd, [(4096 * 130 + 777,)] + SIZES + [(4096 * 25,), (4096 * 20 + 1,)], bits, ty(param),
+                           ty(grad), ty(copy), [0, 1, 4, 16, 0, 8, 0], hp=hp)
+    for t in range(1, 3):
+        for g in opt.grads:
+            g.copy_(spread(torch, gen, g.numel(), 1e-2).view(g.shape))
+        before = snapshot(opt)
+        opt.step(1e-3)
+        check_step(torch, opt, before, t, 1e-3)
+        assert opt.status() == (0, 0)
+    guard.check()
+
+
+@pytest.mark.parametrize("bits", [32, 8])
 @pytest.mark.parametrize("scale", [1e-30, 1e-12, 1e3, 1e15])
 def test_gradient_magnitudes(torch, bd, bits, scale):
     # squares from below fp32's range (they vanish: r = 0) to near its end; a block with one value 1e6 times the
@@ -218,7 +239,7 @@ def test_no_gradient_leaves_zero_moments(torch, bd):
 def test_scalar_and_vector_accesses_give_the_same_bits(torch, bd, bits):
     out = []
     for offset in (0, 1, 4, 16):
-        opt, guard, gen = make(torch, bd, SIZES + [(9000,)], bits, torch.bfloat16, torch.bfloat16, None, offset)
+        opt, guard, gen = make(torch, bd, SIZES + [(9000,), (4096 * 160 + 9,)], bits, torch.bfloat16, torch.bfloat16, None, offset)
         for _ in range(3):
             for g in opt.grads:
                 g.copy_(spread(torch, gen, g.numel(), 1e-2).view(g.shape))
@@ -579,8 +600,8 @@ def test_construction_is_refused_while_capturing(torch, bd):
 
 def test_lists_on_two_streams(torch, bd):
     # two lists stepped at the same time, on streams other than the one that made them
-    pair = [make(torch, bd, [(200000,), (1003,)], 8, torch.bfloat16, torch.bfloat16, None, 0, seed=s) for s in (1, 1)]
-    ref = make(torch, bd, [(200000,), (1003,)], 8, torch.bfloat16, torch.bfloat16, None, 0, seed=1)[0]
+    pair = [make(torch, bd, [(700000,), (1003,)], 8, torch.bfloat16, torch.bfloat16, None, 0, seed=s) for s in (1, 1)]
+    ref = make(torch, bd, [(700000,), (1003,)], 8, torch.bfloat16, torch.bfloat16, None, 0, seed=1)[0]
     x = [torch.randn(g.shape, generator=pair[0][2]) for g in ref.grads]
     for o in (ref, pair[0][0], pair[1][0]):
         for g, y in zip(o.grads, x):
@@ -651,11 +672,11 @@ def test_binding_refuses(torch, bd):
 # ---------------------------------------------------------------- bits
 
 @pytest.mark.parametrize("bits", [32, 8])
-def test_moments_are_those_of_fp32_rounded_operation_by_operation(torch, bd, bits):
+@pytest.mark.parametrize("shapes", [[(40000,), (5001,)], [(700000,), (5001,)]])
+def test_moments_are_those_of_fp32_rounded_operation_by_operation(torch, bd, bits, shapes):
     # the moments' products and sums are rounded one by one, and 8-bit roots correctly: numpy's fp32 has the same
     # bits, and with them the same codes
     f = np.float32
-    shapes = [(40000,), (5001,)]
     opt, guard, gen = make(torch, bd, shapes, bits, torch.float32, torch.float32, None, 0)
     b1, b2 = f(opt.hp.beta1), f(opt.hp.beta2)
     for t in range(1, 6):
@@ -725,7 +746,7 @@ def test_counter_goes_on_from_a_late_step(torch, bd):
 
 def test_waits_for_tiles_are_bounded(torch, bd):
     # the loads of one step are withheld: its waits run out, the launch ends and says so, and the next step is whole
-    p, g = torch.ones(4096 * 3 + 5, device="cuda"), torch.ones(4096 * 3 + 5, device="cuda")
+    p, g = torch.ones(4096 * 200 + 5, device="cuda"), torch.ones(4096 * 200 + 5, device="cuda")
     opt = bd.AdamW([p], [g], state_bits=8, weight_decay=0.0)
     assert bd.load().shampoo_debug_inject_timeout() == 0
     opt.step(1e-2)
