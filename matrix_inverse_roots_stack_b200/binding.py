@@ -391,7 +391,7 @@ class _TensorList:
     def _adopt(self, ctx, ws_bytes, owned):
         import torch
         self._ctx = ctx
-        self._cuda = torch.cuda
+        self._cuda, self._device = torch.cuda, torch.cuda.current_device
         self._index = self.device.index
         self.ws = _workspace(ws_bytes, self.device)
         self._ws_at, self._ws_bytes = self.ws.data_ptr(), self.ws.numel()
@@ -420,16 +420,15 @@ class _TensorList:
             self._streams.add(raw)
         return raw
 
-    def _run(self, name, *args):
+    def _run(self, fn, *args):
         """A library call, on the list's device."""
-        fn = getattr(_lib, name)
-        if self._cuda.current_device() == self._index:
+        if self._device() == self._index:
             rc = fn(*args)
         else:
             with self._cuda.device(self.device):
                 rc = fn(*args)
-        if rc != SHAMPOO_OK:
-            raise ShampooError(rc, name)
+        if rc:
+            raise ShampooError(rc, fn.__name__)
 
     def status(self, stream=None):
         """Synchronise and return (code, flags) of the last call."""
@@ -467,19 +466,20 @@ class GradClip(_TensorList):
         self.out = torch.zeros(2, dtype=torch.float32, device=self.device)
         self._out_at = self.out.data_ptr()
         self._adopt(ctx, nbytes.value, [self.out])
-        self._run("shampoo_grads_bind", ctx, self._ws_at, self._ws_bytes, self._on(None))
+        self._norm, self._clip = _lib.shampoo_grad_norm, _lib.shampoo_grad_clip
+        self._run(_lib.shampoo_grads_bind, ctx, self._ws_at, self._ws_bytes, self._on(None))
         torch.cuda.current_stream(self.device).synchronize()  # ready for any stream
 
     def norm(self, max_norm=float("inf"), inv_scale=1.0, stream=None):
         """Fill and return :attr:`out`; the gradients are only read."""
-        self._run("shampoo_grad_norm", self._ctx, max_norm, inv_scale, self._out_at, self._ws_at, self._ws_bytes,
+        self._run(self._norm, self._ctx, max_norm, inv_scale, self._out_at, self._ws_at, self._ws_bytes,
                   self._on(stream))
         return self.out
 
     def clip(self, max_norm, inv_scale=1.0, stream=None):
         """:meth:`norm`, then every gradient times coef, in place (zero where
         coef is NaN)."""
-        self._run("shampoo_grad_clip", self._ctx, max_norm, inv_scale, self._out_at, self._ws_at, self._ws_bytes,
+        self._run(self._clip, self._ctx, max_norm, inv_scale, self._out_at, self._ws_at, self._ws_bytes,
                   self._on(stream))
         return self.out
 
@@ -568,7 +568,9 @@ class AdamW(_TensorList):
         self.moment_elems = elems.value
         self._adopt(ctx, nbytes.value, owned)
         self._dtypes = {f32: DTYPE_F32, bf16: DTYPE_BF16}
-        self._run("shampoo_adamw_bind", ctx, steps_taken, self._ws_at, self._ws_bytes, self._on(None))
+        self._step = _lib.shampoo_adamw_step
+        self._read, self._load = _lib.shampoo_adamw_read_moments, _lib.shampoo_adamw_load_moments
+        self._run(_lib.shampoo_adamw_bind, ctx, steps_taken, self._ws_at, self._ws_bytes, self._on(None))
         torch.cuda.current_stream(dev).synchronize()  # ready for any stream
 
     def step(self, lr=1e-3, coef=None, step=0, stream=None):
@@ -577,32 +579,32 @@ class AdamW(_TensorList):
         the device that multiplies the gradients (``GradClip.out[1:]``); where
         it is not finite the step is not taken.  step: this step's number, or
         0 to continue the counter on the device."""
-        lr_at = coef_at = None
-        if hasattr(lr, "data_ptr"):
-            lr, lr_at, held = 0.0, self._scalar(lr, "lr"), lr
-        else:
-            lr, held = float(lr), None
+        held = lr_at = coef_at = None
+        if type(lr) is not float:
+            if hasattr(lr, "data_ptr"):
+                lr, lr_at, held = 0.0, self._scalar(lr, "lr"), lr
+            else:
+                lr = float(lr)
         if coef is not None:
             coef_at = self._scalar(coef, "coef")
-        self._run("shampoo_adamw_step", self._ctx, step, lr, lr_at, coef_at, self._ws_at, self._ws_bytes,
+        self._run(self._step, self._ctx, step, lr, lr_at, coef_at, self._ws_at, self._ws_bytes,
                   self._on(stream, held, coef))
 
     def steps_taken(self, stream=None):
         """Synchronise and read the step counter."""
         t = ctypes.c_int(0)
-        self._run("shampoo_adamw_steps_taken", self._ctx, self._ws_at, self._ws_bytes, self._on(stream),
+        self._run(_lib.shampoo_adamw_steps_taken, self._ctx, self._ws_at, self._ws_bytes, self._on(stream),
                   ctypes.byref(t))
         return t.value
 
     def _scalar(self, t, what):
-        if t.dtype not in self._dtypes or self._dtypes[t.dtype] != DTYPE_F32 or t.numel() != 1 or \
-                t.device != self.device:
+        if self._dtypes.get(t.dtype) != DTYPE_F32 or t.numel() != 1 or t.get_device() != self._index:
             raise ValueError(f"{what} must be one fp32 value on {self.device}")
         return t.data_ptr()
 
     def _flat(self, t, what):
         if t.dtype not in self._dtypes or t.numel() != self.moment_elems or not t.is_contiguous() or \
-                t.device != self.device:
+                t.get_device() != self._index:
             raise ValueError(f"{what} must be {self.moment_elems} contiguous fp32 or bf16 values on {self.device}")
         return t.data_ptr()
 
@@ -617,15 +619,16 @@ class AdamW(_TensorList):
     def read_moments(self, dtype=None, m=None, v=None, stream=None):
         """Both moments as flat tensors (see :meth:`views`) of fp32 (default)
         or bf16, into m and v where given."""
-        import torch
-        if m is None:
-            m = torch.empty(self.moment_elems, dtype=dtype or torch.float32, device=self.device)
-        if v is None:
-            v = torch.empty(self.moment_elems, dtype=m.dtype, device=self.device)
+        if m is None or v is None:
+            import torch
+            if m is None:
+                m = torch.empty(self.moment_elems, dtype=dtype or torch.float32, device=self.device)
+            if v is None:
+                v = torch.empty(self.moment_elems, dtype=m.dtype, device=self.device)
         m_at, v_at = self._flat(m, "m"), self._flat(v, "v")
         if v.dtype != m.dtype or (dtype is not None and m.dtype != dtype):
             raise ValueError("m and v must be of the one type asked for")
-        self._run("shampoo_adamw_read_moments", self._ctx, m_at, v_at, self._dtypes[m.dtype], self._ws_at,
+        self._run(self._read, self._ctx, m_at, v_at, self._dtypes[m.dtype], self._ws_at,
                   self._ws_bytes, self._on(stream, m, v))
         return m, v
 
@@ -634,5 +637,5 @@ class AdamW(_TensorList):
         m_at, v_at = self._flat(m, "m"), self._flat(v, "v")
         if self._dtypes[m.dtype] != DTYPE_F32 or self._dtypes[v.dtype] != DTYPE_F32:
             raise ValueError("moments are set from fp32 values")
-        self._run("shampoo_adamw_load_moments", self._ctx, m_at, v_at, self._ws_at, self._ws_bytes,
+        self._run(self._load, self._ctx, m_at, v_at, self._ws_at, self._ws_bytes,
                   self._on(stream, m, v))

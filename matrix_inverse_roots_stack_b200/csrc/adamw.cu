@@ -1054,14 +1054,16 @@ __global__ void __launch_bounds__(kReadThreads) read_moments_kernel(const AdamwT
                                                                     int dtype) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const AdamwTensorDev& t = table.tensors[first_tensor(table.first_tile, table.n_tensors, static_cast<int>(blockIdx.x))];
-  const long long first = static_cast<long long>(static_cast<int>(blockIdx.x) - t.first_tile) * kTile + warp * (kReadBlocks * kQBlock);
+  const long long tile0 = static_cast<long long>(static_cast<int>(blockIdx.x) - t.first_tile) * kTile;
+  const long long first = tile0 + warp * kQBlock;
+  constexpr int kNext = kReadThreads / 32 * kQBlock;  // from a warp's block to its next
   f32x2 m[4], v[4];
-  if ((t.flags & kFlagEight) && (t.flags & kFlagVec) && first + kReadBlocks * kQBlock <= t.n) {
+  if ((t.flags & kFlagEight) && (t.flags & kFlagVec) && tile0 + kTile <= t.n) {
     uint2 qm[kReadBlocks], qv[kReadBlocks];
     int ms[kReadBlocks], vs[kReadBlocks];
 #pragma unroll
     for (int w = 0; w < kReadBlocks; ++w) {
-      const long long e0 = first + w * kQBlock;
+      const long long e0 = first + w * kNext;
       qm[w] = *(reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(t.m) + e0) + lane);
       qv[w] = *(reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(t.v) + e0) + lane);
       ms[w] = t.m_scale[e0 >> 8];
@@ -1074,12 +1076,12 @@ __global__ void __launch_bounds__(kReadThreads) read_moments_kernel(const AdamwT
       m8_values4(qm[w].y, mf, m + 2);
       v8_values4(qv[w].x, vf, v);
       v8_values4(qv[w].y, vf, v + 2);
-      write_moments(t, first + w * kQBlock, m, v, false, m_out, v_out, dtype);
+      write_moments(t, first + w * kNext, m, v, false, m_out, v_out, dtype);
     }
     return;
   }
   for (int w = 0; w < kReadBlocks; ++w) {
-    const long long e0 = first + w * kQBlock;
+    const long long e0 = first + w * kNext;
     if (e0 >= t.n) break;
     const int left = static_cast<int>(min(static_cast<long long>(kQBlock), t.n - e0)), i0 = 8 * lane;
     if (t.flags & kFlagEight) {
