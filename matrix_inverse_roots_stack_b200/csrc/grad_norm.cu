@@ -42,6 +42,23 @@ __device__ __forceinline__ void add_squares(const float* x, double* acc) {
   }
 }
 
+// The same for eight bf16 elements as they lie in memory.  An SM converts 16
+// fp32 numbers a clock to fp64, and at two bytes an element that is two thirds
+// of the time; so every other one is made of its bits instead.  bf16's exponent and
+// mantissa, put where fp64 has its own, are |x| 2^-896, subnormals and 0 included.  An
+// exponent of infinity or NaN would pass as a number: 'special' becomes NaN
+// then (the word as an fp32 number has that exponent too).  1.36G elements: 461 -> 441 us.
+__device__ __forceinline__ void add_squares_bf16(const Raw8& r, double* acc, float& special) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const double lo = __uint_as_float(r.w[j] << 16);
+    const double hi = __hiloint2double(static_cast<int>((r.w[j] >> 3) & 0x0fffe000u), 0) * 0x1p896;
+    acc[0] = fma(lo, lo, acc[0]);
+    acc[1] = fma(hi, hi, acc[1]);
+    special = fmaf(__uint_as_float(r.w[j]), 0.0f, special);
+  }
+}
+
 // Sum of a block's values, in a fixed order; valid in thread 0.
 __device__ __forceinline__ double block_sum(double x) {
   __shared__ double part[kListWarps];
@@ -76,6 +93,7 @@ __global__ void __launch_bounds__(kListThreads) grad_norm_kernel(const GradChunk
     unsigned next = 0;  // looked at behind the share
     if (threadIdx.x == 0) next = atomicAdd(&hdr->next, 1u);
     double acc[2] = {0.0, 0.0};
+    float special = 0.0f;
     const int width = gridDim.x, first = p / width * (width * rounds) + p % width;
     for (int j = 0, k = n_chunks - 1 - first; j < rounds && k >= 0; ++j, k -= width) {
       const GradChunk c = chunks[k];
@@ -84,11 +102,16 @@ __global__ void __launch_bounds__(kListThreads) grad_norm_kernel(const GradChunk
         Raw8 r[kSteps];
 #pragma unroll
         for (int s = 0; s < kSteps; ++s) load8(c.grad, (s * kListWarps + warp) * 32 + lane, type, r[s]);
+        if (type == SHAMPOO_DTYPE_BF16) {
 #pragma unroll
-        for (int s = 0; s < kSteps; ++s) {
-          float x[8];
-          widen8(r[s], type, x);
-          add_squares(x, acc);
+          for (int s = 0; s < kSteps; ++s) add_squares_bf16(r[s], acc, special);
+        } else {
+#pragma unroll
+          for (int s = 0; s < kSteps; ++s) {
+            float x[8];
+            widen8(r[s], type, x);
+            add_squares(x, acc);
+          }
         }
       } else {
         for (int b = warp * kQBlock; b < c.count; b += kListWarps * kQBlock) {
@@ -99,7 +122,7 @@ __global__ void __launch_bounds__(kListThreads) grad_norm_kernel(const GradChunk
       }
     }
     if (threadIdx.x == 0) taken = static_cast<int>(gridDim.x + next);
-    const double sum = block_sum(acc[0] + acc[1]);  // with barriers: 'taken' is there
+    const double sum = block_sum(acc[0] + acc[1] + special);  // with barriers: 'taken' is there
     if (threadIdx.x == 0) partial[p] = sum;
     p = taken;
     __syncthreads();

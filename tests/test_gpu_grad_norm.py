@@ -118,6 +118,32 @@ def test_non_finite(torch, bd, bad, dtype):
     assert clip.norm(1.0).tolist() == [0.0, 1.0] and clip.status() == (0, 0)
 
 
+@pytest.mark.parametrize("dtype", ["float32", "bfloat16", "float16"])
+def test_non_finite_at_any_place_of_a_whole_chunk(torch, bd, dtype):
+    g = torch.ones(8192 * 3, dtype=getattr(torch, dtype), device="cuda")
+    clip = bd.GradClip([g])
+    for at in (0, 1, 2, 7, 255, 256, 8190, 8191, 8192, 3 * 8192 - 2, 3 * 8192 - 1):
+        for bad in (float("nan"), float("inf"), -float("inf")):
+            g[at] = bad
+            norm, coef = clip.norm(1.0).tolist()
+            assert not math.isfinite(norm) and math.isnan(coef) and clip.status()[0] == bd.SHAMPOO_ENONFINITE
+        g[at] = 1.0
+    n = math.sqrt(8192 * 3)
+    assert clip.norm()[0].item() == np.float32(n) and clip.status() == (0, 0)
+
+
+@pytest.mark.parametrize("values", [(1e-39, 9.2e-41), (1e-39, 0.0), (0.0, 1e-39), (3e38, 1.0), (1.0, 3e38),
+                                    (-1e-20, 1e-20), (0.0, 0.0), (-2.5, 1e-30)])
+def test_bf16_values_of_any_size(torch, bd, values):
+    # even and odd elements are converted differently: subnormal, zero and near the largest, in both places
+    g = torch.tensor(values, device="cuda").to(torch.bfloat16).repeat(8192)
+    clip = bd.GradClip([g])
+    n = math.sqrt(float(g.double().square().sum()))
+    norm = clip.norm(1e30)[0].item()
+    assert clip.status() == (0, 0)
+    assert norm == math.inf if n > 3.4028235e38 else abs(norm - n) <= 1.01 * H * n + 2.0 ** -150
+
+
 def test_captured_clip_replays(torch, bd):
     grads = grads_of(torch, [100003, 77], torch.float32, 0)
     twin = [g.clone() for g in grads]
