@@ -928,49 +928,57 @@ __global__ void __launch_bounds__(kDirectThreads) adamw_direct_kernel(const Adam
 
 // From flat fp32 moments into the list's own: 8-bit tensors are rounded to
 // nearest, 32-bit ones copied.  One block of threads to a tile, here and
-// below.
+// below; a warp has two blocks and asks for both before it uses either.
+constexpr int kLoadBlocks = kTileBlocks / kListWarps;
+
 __global__ void __launch_bounds__(kListThreads) load_moments_kernel(const AdamwTable table, AdamwHeader* hdr,
                                                                     const float* __restrict__ m_in,
                                                                     const float* __restrict__ v_in) {
   const int lane = threadIdx.x & 31;
   const AdamwTensorDev& t = table.tensors[first_tensor(table.first_tile, table.n_tensors, static_cast<int>(blockIdx.x))];
-  const long long tile0 = static_cast<long long>(static_cast<int>(blockIdx.x) - t.first_tile) * kTile;
-  bool bad = false;
+  const long long first = static_cast<long long>(static_cast<int>(blockIdx.x) - t.first_tile) * kTile +
+                          (threadIdx.x >> 5) * kQBlock;
+  const long long flat = static_cast<long long>(t.first) * kQBlock;
+  const bool vec = t.flags & kFlagVec, eight = t.flags & kFlagEight;
+  float m[kLoadBlocks][8], v[kLoadBlocks][8];
 #pragma unroll
-  for (int w = 0; w < kTileBlocks / kListWarps; ++w) {
-    const long long e0 = tile0 + ((threadIdx.x >> 5) + w * kListWarps) * kQBlock;
-    if (e0 >= t.n) break;
-    const long long flat = static_cast<long long>(t.first) * kQBlock + e0;
-    const int left = static_cast<int>(min(static_cast<long long>(kQBlock), t.n - e0));
-    const bool vec = (t.flags & kFlagVec) && left == kQBlock;
-    const int i0 = vec ? 8 * lane : lane;
-    const float* fm = m_in + flat;
-    const float* fv = v_in + flat;
-    float m[8], v[8], r[8];
-    if (vec) {
+  for (int w = 0; w < kLoadBlocks; ++w) {
+    const long long e0 = first + w * (kListWarps * kQBlock);
+    const float* fm = m_in + flat + e0;
+    const float* fv = v_in + flat + e0;
+    if (vec && e0 + kQBlock <= t.n) {
       Raw8 rm, rv;
-      load32B(fm + i0, rm.w);
-      load32B(fv + i0, rv.w);
+      load32B(fm + 8 * lane, rm.w);
+      load32B(fv + 8 * lane, rv.w);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) m[j] = __uint_as_float(rm.w[j]), v[j] = __uint_as_float(rv.w[j]);
+      for (int j = 0; j < 8; ++j) m[w][j] = __uint_as_float(rm.w[j]), v[w][j] = __uint_as_float(rv.w[j]);
     } else {
+      const int left = static_cast<int>(min(static_cast<long long>(kQBlock), max(t.n - e0, 0ll)));
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        const bool in = i0 + 32 * j < left;
-        m[j] = in ? fm[i0 + 32 * j] : 0.0f;
-        v[j] = in ? fv[i0 + 32 * j] : 0.0f;
+        const bool in = lane + 32 * j < left;
+        m[w][j] = in ? fm[lane + 32 * j] : 0.0f;
+        v[w][j] = in ? fv[lane + 32 * j] : 0.0f;
       }
     }
-    float mmax = 0.0f, rmax = 0.0f;
+  }
+  bool bad = false;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) r[j] = __fsqrt_rn(v[j]);
+  for (int w = 0; w < kLoadBlocks; ++w) {
+    const long long e0 = first + w * (kListWarps * kQBlock);
+    if (e0 >= t.n) break;
+    const bool whole = vec && e0 + kQBlock <= t.n;
+    const int left = static_cast<int>(min(static_cast<long long>(kQBlock), t.n - e0));
+    float mmax = 0.0f, rmax = 0.0f, r[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) r[j] = __fsqrt_rn(v[w][j]);
 #pragma unroll
     for (int j = 0; j < 8; j += 2) {
-      mmax = max_abs3(mmax, m[j], m[j + 1]);
+      mmax = max_abs3(mmax, m[w][j], m[w][j + 1]);
       rmax = max_abs3(rmax, r[j], r[j + 1]);
     }
     bad |= not_finite(max_abs3(mmax, rmax, 0.0f));
-    if (t.flags & kFlagEight) {
+    if (eight) {
       uint8_t* cm = static_cast<uint8_t*>(t.m) + e0;
       uint8_t* cv = static_cast<uint8_t*>(t.v) + e0;
       mmax = warp_max(mmax);
@@ -981,9 +989,9 @@ __global__ void __launch_bounds__(kListThreads) load_moments_kernel(const AdamwT
       unsigned ca[8], cb[8];
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        const unsigned x = __float_as_uint(__fmul_rn(__fmul_rn(m[j], mu), kM8Down));
+        const unsigned x = __float_as_uint(__fmul_rn(__fmul_rn(m[w][j], mu), kM8Down));
         const unsigned y = __float_as_uint(__fmul_rn(__fmul_rn(r[j], vu), kV8Down));
-        ca[j] = m8_code(x, m[j], nearest_even(x, kM8Shift));
+        ca[j] = m8_code(x, m[w][j], nearest_even(x, kM8Shift));
         cb[j] = v8_code(y, nearest_even(y, kV8Shift));
       }
       const uint2 am = make_uint2(top_bytes(ca[0], ca[1], ca[2], ca[3]), top_bytes(ca[4], ca[5], ca[6], ca[7]));
@@ -997,29 +1005,29 @@ __global__ void __launch_bounds__(kListThreads) load_moments_kernel(const AdamwT
         t.m_scale[e0 >> 8] = mi.byte(mmax);
         t.v_scale[e0 >> 8] = vi.byte(rmax);
       }
-      if (vec) {
+      if (whole) {
         *(reinterpret_cast<uint2*>(cm) + lane) = am;
         *(reinterpret_cast<uint2*>(cv) + lane) = bv;
       } else {
 #pragma unroll
         for (int j = 0; j < 8; ++j)
-          if (i0 + 32 * j < left) {
-            cm[i0 + 32 * j] = static_cast<uint8_t>((j < 4 ? am.x : am.y) >> (8 * (j & 3)));
-            cv[i0 + 32 * j] = static_cast<uint8_t>((j < 4 ? bv.x : bv.y) >> (8 * (j & 3)));
+          if (lane + 32 * j < left) {
+            cm[lane + 32 * j] = static_cast<uint8_t>((j < 4 ? am.x : am.y) >> (8 * (j & 3)));
+            cv[lane + 32 * j] = static_cast<uint8_t>((j < 4 ? bv.x : bv.y) >> (8 * (j & 3)));
           }
       }
     } else {
       float* om = static_cast<float*>(t.m) + e0;
       float* ov = static_cast<float*>(t.v) + e0;
-      if (vec) {
-        store8(om, lane, SHAMPOO_DTYPE_F32, m);
-        store8(ov, lane, SHAMPOO_DTYPE_F32, v);
+      if (whole) {
+        store8(om, lane, SHAMPOO_DTYPE_F32, m[w]);
+        store8(ov, lane, SHAMPOO_DTYPE_F32, v[w]);
       } else {
 #pragma unroll
         for (int j = 0; j < 8; ++j)
-          if (i0 + 32 * j < left) {
-            om[i0 + 32 * j] = m[j];
-            ov[i0 + 32 * j] = v[j];
+          if (lane + 32 * j < left) {
+            om[lane + 32 * j] = m[w][j];
+            ov[lane + 32 * j] = v[w][j];
           }
       }
     }

@@ -43,7 +43,7 @@ def grads_of(torch, sizes, dtype, offset, seed=0, std=1e-2):
     return out
 
 
-SIZES = [[1], [0, 7, 0], [8191, 8192, 8193], [1, 255, 256, 257, 100003], [3_000_001]]
+SIZES = [[1], [0, 7, 0], [8191, 8192, 8193], [16383, 16384, 16385], [1, 255, 256, 257, 100003], [3_000_001]]
 
 
 @pytest.mark.parametrize("sizes", SIZES)
@@ -120,15 +120,15 @@ def test_non_finite(torch, bd, bad, dtype):
 
 @pytest.mark.parametrize("dtype", ["float32", "bfloat16", "float16"])
 def test_non_finite_at_any_place_of_a_whole_chunk(torch, bd, dtype):
-    g = torch.ones(8192 * 3, dtype=getattr(torch, dtype), device="cuda")
+    g = torch.ones(16384 * 3, dtype=getattr(torch, dtype), device="cuda")
     clip = bd.GradClip([g])
-    for at in (0, 1, 2, 7, 255, 256, 8190, 8191, 8192, 3 * 8192 - 2, 3 * 8192 - 1):
+    for at in (0, 1, 2, 7, 255, 256, 8190, 8191, 8192, 16383, 16384, 3 * 16384 - 2, 3 * 16384 - 1):
         for bad in (float("nan"), float("inf"), -float("inf")):
             g[at] = bad
             norm, coef = clip.norm(1.0).tolist()
             assert not math.isfinite(norm) and math.isnan(coef) and clip.status()[0] == bd.SHAMPOO_ENONFINITE
         g[at] = 1.0
-    n = math.sqrt(8192 * 3)
+    n = math.sqrt(16384 * 3)
     assert clip.norm()[0].item() == np.float32(n) and clip.status() == (0, 0)
 
 
