@@ -373,8 +373,9 @@ def _dtype_code(t):
 def _check_list(tensors, what, dtypes, device, like=None):
     """Contiguous CUDA tensors of one device and of the given types; `like`:
     tensors whose shapes they have."""
+    index = device.index
     for i, t in enumerate(tensors):
-        if t.dtype not in dtypes or not t.is_cuda or t.device != device or not t.is_contiguous():
+        if t.dtype not in dtypes or t.get_device() != index or not t.is_contiguous():
             raise ValueError(f"{what}[{i}] must be a contiguous tensor on {device} of type "
                              f"{' or '.join(str(d) for d in dtypes)}")
         if like is not None and t.shape != like[i].shape:
@@ -526,42 +527,45 @@ class AdamW(_TensorList):
         _check_list(self.params, "params", (f32, bf16), dev)
         _check_list(self.grads, "grads", (f32, bf16, f16), dev, self.params)
         owned = []
+        sizes = [p.numel() for p in self.params]
+        eight = [b == 8 for b in self.state_bits]
 
-        def state(given, what, dtype, numel):
-            out = []
-            given = each(given, what)
-            for i, t in enumerate(given):
-                want = numel(i)
+        def state(given, what, types, numels):
+            """The given moments or scales, checked, or zeros; None where a
+            parameter has none."""
+            out = each(given, what)
+            for i, (t, dtype, numel) in enumerate(zip(out, types, numels)):
                 if t is None:
-                    t = torch.zeros(want, dtype=dtype(i), device=dev) if want is not None else None
-                    owned.extend([t] if t is not None else [])
-                elif want is None:
+                    if numel is not None:
+                        out[i] = torch.zeros(numel, dtype=dtype, device=dev)
+                        owned.append(out[i])
+                elif numel is None:
                     raise ValueError(f"{what}[{i}] is for 8-bit moments only")
-                elif t.numel() != want:
-                    raise ValueError(f"{what}[{i}] has {t.numel()} elements, not {want}")
-                else:
-                    _check_list([t], what, (dtype(i),), dev)
-                out.append(t)
+                elif t.numel() != numel:
+                    raise ValueError(f"{what}[{i}] has {t.numel()} elements, not {numel}")
+                elif t.dtype != dtype:
+                    raise ValueError(f"{what}[{i}] must be of type {dtype}")
+            _check_list([t for t in out if t is not None], what, (f32, torch.uint8), dev)
             return out
 
-        codes = lambda i: torch.uint8 if self.state_bits[i] == 8 else f32
-        blocks = lambda i: -(-self.params[i].numel() // QBLOCK) if self.state_bits[i] == 8 else None
-        self.m = state(m, "m", codes, lambda i: self.params[i].numel())
-        self.v = state(v, "v", codes, lambda i: self.params[i].numel())
-        self.m_scale = state(m_scale, "m_scale", lambda i: torch.uint8, blocks)
-        self.v_scale = state(v_scale, "v_scale", lambda i: torch.uint8, blocks)
-        arr = (AdamwTensor * n)()
-        for i, p in enumerate(self.params):
-            c = self.copies[i]
-            if c is not None:
-                if p.dtype != f32:
-                    raise ValueError(f"copies[{i}] is for an fp32 parameter only")
-                _check_list([c], "copies", (bf16, f16), dev, [p])
-            at = lambda t: None if t is None else t.data_ptr()
-            arr[i] = AdamwTensor(p.numel(), p.data_ptr(), self.grads[i].data_ptr(), at(c), at(self.m[i]),
-                                 at(self.v[i]), at(self.m_scale[i]), at(self.v_scale[i]), _dtype_code(p),
-                                 _dtype_code(self.grads[i]), DTYPE_F32 if c is None else _dtype_code(c),
-                                 self.state_bits[i], lr_scale[i], weight_decay[i])
+        codes = [torch.uint8 if e else f32 for e in eight]
+        bytes_ = [torch.uint8] * n
+        blocks = [-(-k // QBLOCK) if e else None for k, e in zip(sizes, eight)]
+        self.m, self.v = state(m, "m", codes, sizes), state(v, "v", codes, sizes)
+        self.m_scale = state(m_scale, "m_scale", bytes_, blocks)
+        self.v_scale = state(v_scale, "v_scale", bytes_, blocks)
+        given = [(i, c) for i, c in enumerate(self.copies) if c is not None]
+        if any(self.params[i].dtype != f32 for i, _ in given):
+            raise ValueError("copies are for fp32 parameters only")
+        _check_list([c for _, c in given], "copies", (bf16, f16), dev, [self.params[i] for i, _ in given])
+        code = {f32: DTYPE_F32, bf16: DTYPE_BF16, f16: DTYPE_F16}
+        at = lambda t: None if t is None else t.data_ptr()
+        arr = (AdamwTensor * n)(*[
+            (k, p.data_ptr(), g.data_ptr(), at(c), m_.data_ptr(), v_.data_ptr(), at(ms), at(vs), code[p.dtype],
+             code[g.dtype], DTYPE_F32 if c is None else code[c.dtype], b, ls, wd)
+            for k, p, g, c, m_, v_, ms, vs, b, ls, wd in zip(sizes, self.params, self.grads, self.copies, self.m, self.v,
+                                                             self.m_scale, self.v_scale, self.state_bits, lr_scale,
+                                                             weight_decay)])
         ctx, nbytes, elems = ctypes.c_void_p(), ctypes.c_size_t(0), ctypes.c_int64(0)
         _check(load().shampoo_adamw_init(ctypes.byref(ctx), arr, n, ctypes.byref(self.hp), ctypes.byref(nbytes),
                                          ctypes.byref(elems)), "shampoo_adamw_init")
