@@ -325,11 +325,12 @@ SHAMPOO_API void shampoo_destroy(shampoo_ctx* ctx);
  * A list is described once (..._init, host only), and its table is uploaded
  * to the caller's workspace once (..._bind, 256-byte aligned); the tensors'
  * addresses then stay fixed, and their contents may change between calls.
- * All other calls take the same workspace (SHAMPOO_EINVAL for another one),
- * are stream-ordered and can be captured into a CUDA graph; bind cannot
- * (SHAMPOO_EINVAL on a capturing stream).  Calls on one workspace must not
- * overlap.  The workspace's first word is the status word of its last norm,
- * clip, step or load call (shampoo_read_status).
+ * All other calls take the same workspace (SHAMPOO_EINVAL for another one, and
+ * for a device scalar that is not aligned to its 4 bytes), are stream-ordered
+ * and can be captured into a CUDA graph; bind cannot (SHAMPOO_EINVAL on a
+ * capturing stream).  Calls on one workspace must not overlap.  The
+ * workspace's first word is the status word of its last norm, clip, step or
+ * load call (shampoo_read_status).
  * ---------------------------------------------------------------------- */
 
 #define SHAMPOO_DTYPE_F32 0

@@ -389,14 +389,17 @@ class _TensorList:
 
     _destroy = None
 
-    def _adopt(self, ctx, ws_bytes, owned):
+    def _adopt(self, ctx, ws_bytes, held):
+        """held: every tensor that the list's calls work on.  Those that the
+        caller made are, as with torch's own operations, taken to be the
+        current stream's."""
         import torch
         self._ctx = ctx
         self._cuda, self._device = torch.cuda, torch.cuda.current_device
         self._index = self.device.index
         self.ws = _workspace(ws_bytes, self.device)
         self._ws_at, self._ws_bytes = self.ws.data_ptr(), self.ws.numel()
-        self._owned = [self.ws] + owned
+        self._held = [self.ws] + held
         self._streams = {torch.cuda.current_stream(self.device).cuda_stream}
         # the current stream's handle, without an object around it where torch offers that
         raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
@@ -415,8 +418,8 @@ class _TensorList:
                 if t is not None:
                     t.record_stream(stream)
         if raw not in self._streams:
-            # memory made here is not handed out again before this stream is done with it
-            for t in self._owned:
+            # the list's memory is not handed out again before this stream is done with it
+            for t in self._held:
                 t.record_stream(self._cuda.current_stream(self.device) if stream is None else stream)
             self._streams.add(raw)
         return raw
@@ -466,7 +469,7 @@ class GradClip(_TensorList):
                "shampoo_grads_init")
         self.out = torch.zeros(2, dtype=torch.float32, device=self.device)
         self._out_at = self.out.data_ptr()
-        self._adopt(ctx, nbytes.value, [self.out])
+        self._adopt(ctx, nbytes.value, self.grads + [self.out])
         self._norm, self._clip = _lib.shampoo_grad_norm, _lib.shampoo_grad_clip
         self._run(_lib.shampoo_grads_bind, ctx, self._ws_at, self._ws_bytes, self._on(None))
         torch.cuda.current_stream(self.device).synchronize()  # ready for any stream
@@ -526,7 +529,6 @@ class AdamW(_TensorList):
             raise ValueError(f"{len(self.grads)} gradients for {n} parameters")
         _check_list(self.params, "params", (f32, bf16), dev)
         _check_list(self.grads, "grads", (f32, bf16, f16), dev, self.params)
-        owned = []
         sizes = [p.numel() for p in self.params]
         eight = [b == 8 for b in self.state_bits]
 
@@ -538,7 +540,6 @@ class AdamW(_TensorList):
                 if t is None:
                     if numel is not None:
                         out[i] = torch.zeros(numel, dtype=dtype, device=dev)
-                        owned.append(out[i])
                 elif numel is None:
                     raise ValueError(f"{what}[{i}] is for 8-bit moments only")
                 elif t.numel() != numel:
@@ -570,7 +571,8 @@ class AdamW(_TensorList):
         _check(load().shampoo_adamw_init(ctypes.byref(ctx), arr, n, ctypes.byref(self.hp), ctypes.byref(nbytes),
                                          ctypes.byref(elems)), "shampoo_adamw_init")
         self.moment_elems = elems.value
-        self._adopt(ctx, nbytes.value, owned)
+        held = self.params + self.grads + self.copies + self.m + self.v + self.m_scale + self.v_scale
+        self._adopt(ctx, nbytes.value, [t for t in held if t is not None])
         self._dtypes = {f32: DTYPE_F32, bf16: DTYPE_BF16}
         self._step = _lib.shampoo_adamw_step
         self._read, self._load = _lib.shampoo_adamw_read_moments, _lib.shampoo_adamw_load_moments

@@ -212,7 +212,8 @@ int shampoo_adamw_step(shampoo_adamw* c, int step, float lr, const float* lr_dev
                        size_t ws_bytes, void* stream) {
   const int rc = check_bound(c, ws, ws_bytes);
   if (rc) return rc;
-  if (step < 0 || (!lr_device && !std::isfinite(lr))) return SHAMPOO_EINVAL;
+  if (step < 0 || (!lr_device && !std::isfinite(lr)) || !dash::aligned_to(lr_device, 4) || !dash::aligned_to(coef, 4))
+    return SHAMPOO_EINVAL;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   dash::AdamwArgs a{};
   a.beta1 = make_float2(c->hp.beta1, c->hp.beta1);

@@ -221,7 +221,8 @@ constexpr int kMaxShares = 1 << 15;  // partial sums kept in the workspace
 
 int norm_pass(shampoo_grads* c, float max_norm, float inv_scale, float* out, void* ws, size_t ws_bytes, void* stream,
               bool clip) {
-  if (!c || !out || !(max_norm > 0.0f) || !(inv_scale > 0.0f) || !std::isfinite(inv_scale)) return SHAMPOO_EINVAL;
+  if (!c || !out || !dash::aligned_to(out, 4) || !(max_norm > 0.0f) || !(inv_scale > 0.0f) || !std::isfinite(inv_scale))
+    return SHAMPOO_EINVAL;
   if (!ws || ws_bytes < c->total) return SHAMPOO_EWORKSPACE;
   if (ws != c->bound_ws) return SHAMPOO_EINVAL;
   char* w = static_cast<char*>(ws);
@@ -229,8 +230,8 @@ int norm_pass(shampoo_grads* c, float max_norm, float inv_scale, float* out, voi
   const auto* table = reinterpret_cast<const dash::GradChunk*>(w + dash::kHeaderBytes);
   const int n = static_cast<int>(c->chunks.size());
   dash::grad_norm_kernel<<<c->grid, dash::kListThreads, 0, st>>>(
-      table, n, c->shares, c->rounds, reinterpret_cast<dash::NormHeader*>(w), reinterpret_cast<double*>(w + c->off_partial), max_norm,
-      inv_scale, out);
+      table, n, c->shares, c->rounds, reinterpret_cast<dash::NormHeader*>(w),
+      reinterpret_cast<double*>(w + c->off_partial), max_norm, inv_scale, out);
   dash::prof_count_launch();
   if (cudaGetLastError() != cudaSuccess) return SHAMPOO_ECUDA;
   if (clip && n > 0) {

@@ -619,6 +619,31 @@ def test_lists_on_two_streams(torch, bd):
         guard.check()
 
 
+def test_memory_is_not_handed_out_while_a_stream_uses_it(torch, bd):
+    # tensors of the current stream, stepped on another one that is behind; then everything is dropped
+    side, n = torch.cuda.Stream(), 300000
+    for own in (False, True):  # moments made by the caller, or by the list
+        p, g = torch.ones(n, device="cuda"), torch.ones(n, device="cuda")
+        m = v = None
+        if own:
+            m, v = torch.zeros(n, device="cuda"), torch.zeros(n, device="cuda")
+        opt, clip = bd.AdamW([p], [g], m=m, v=v), bd.GradClip([g])
+        clip.clip(1.0)  # both are loaded then
+        opt.step(1e-3)
+        torch.cuda.synchronize()
+        used = {t.data_ptr() for t in [p, g] + opt.m + opt.v}
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(200_000_000)  # 0.1 s
+            clip.clip(1.0)
+            opt.step(1e-3)
+        del p, g, m, v, opt, clip
+        new = [torch.empty(n, device="cuda") for _ in range(8)]
+        assert not side.query(), "the stream has to be behind still"
+        assert not used & {t.data_ptr() for t in new}
+        torch.cuda.synchronize()
+        del new
+
+
 # ---------------------------------------------------------------- refusals
 
 def test_binding_refuses(torch, bd):
@@ -656,6 +681,10 @@ def test_binding_refuses(torch, bd):
               lambda: opt.load_moments(z(520)[1:513], z(512))):
         with pytest.raises(bd.ShampooError):
             f()
+    scalar = z(2)
+    for at in ((None, scalar.data_ptr() + 2), (scalar.data_ptr() + 1, None)):  # a rate or coefficient off 4 bytes
+        assert bd.load().shampoo_adamw_step(opt._ctx, 0, 1e-3, *at, opt.ws.data_ptr(), opt.ws.numel(), None) == \
+            bd.SHAMPOO_EINVAL
     for f in (lambda: opt.step(1e-3, coef=z(2)), lambda: opt.step(z(1, dtype=torch.bfloat16)),
               lambda: opt.step(1e-3, coef=z(1).cpu()), lambda: opt.load_moments(z(300), z(300)),
               lambda: opt.read_moments(torch.float16), lambda: opt.read_moments(m=z(512), v=z(300)),

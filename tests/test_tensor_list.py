@@ -64,6 +64,7 @@ def test_gradient_calls_validate_before_device_work(lib):
         for max_norm, inv_scale in ((0.0, 1.0), (-1.0, 1.0), (float("nan"), 1.0), (1.0, 0.0), (1.0, -1.0),
                                     (1.0, float("inf")), (1.0, float("nan"))):
             assert fn(ctx, max_norm, inv_scale, out, ws, need, None) == bd.SHAMPOO_EINVAL
+        assert fn(ctx, 1.0, 1.0, ctypes.c_void_p(0x2002), None, need, None) == bd.SHAMPOO_EINVAL  # out off 4 bytes
     lib.shampoo_grads_destroy(ctx)
     lib.shampoo_grads_destroy(None)
 
