@@ -624,13 +624,22 @@ class AdamW(_TensorList):
 
     def read_moments(self, dtype=None, m=None, v=None, stream=None):
         """Both moments as flat tensors (see :meth:`views`) of fp32 (default)
-        or bf16, into m and v where given."""
+        or bf16, into m and v where given.  Those that are not given are made
+        on `stream`: other streams wait for it before they use them."""
         if m is None or v is None:
             import torch
-            if m is None:
-                m = torch.empty(self.moment_elems, dtype=dtype or torch.float32, device=self.device)
-            if v is None:
-                v = torch.empty(self.moment_elems, dtype=m.dtype, device=self.device)
+            made = []
+            # not from the current stream's memory: what was freed there may be in its queued work's use still
+            with torch.cuda.stream(stream):
+                if m is None:
+                    m = torch.empty(self.moment_elems, dtype=dtype or torch.float32, device=self.device)
+                    made.append(m)
+                if v is None:
+                    v = torch.empty(self.moment_elems, dtype=m.dtype, device=self.device)
+                    made.append(v)
+            if stream is not None:  # the caller's stream uses them next
+                for t in made:
+                    t.record_stream(torch.cuda.current_stream(self.device))
         m_at, v_at = self._flat(m, "m"), self._flat(v, "v")
         if v.dtype != m.dtype or (dtype is not None and m.dtype != dtype):
             raise ValueError("m and v must be of the one type asked for")

@@ -644,6 +644,42 @@ def test_memory_is_not_handed_out_while_a_stream_uses_it(torch, bd):
         del new
 
 
+@pytest.mark.parametrize("dtype", ["float32", "bfloat16"])
+def test_moments_read_and_loaded_on_another_stream(torch, bd, dtype):
+    # the current stream is behind, with a dropped temporary of the outputs' size still in its use
+    n, side, dtype = 300000, torch.cuda.Stream(), getattr(torch, dtype)
+    opt = bd.AdamW([torch.zeros(n, device="cuda")], [torch.zeros(n, device="cuda")], state_bits=8)
+    m = torch.randn(opt.moment_elems, generator=torch.Generator("cuda").manual_seed(1), device="cuda")
+    v = m.square()
+    opt.load_moments(m, v)
+    want = opt.read_moments(dtype)
+    doubled = [t * 2 for t in want]
+    temps = [torch.full((opt.moment_elems,), 5.0, dtype=dtype, device="cuda") for _ in "mv"]
+    torch.cuda.synchronize()  # every kernel has run once: loading one would wait for the device
+    torch.cuda._sleep(200_000_000)  # 0.1 s
+    for t in temps:
+        t.fill_(7.0)
+    used = {t.data_ptr() for t in temps}
+    del temps, t
+    opt.load_moments(m, v, stream=side)
+    got = opt.read_moments(dtype, stream=side)
+    assert not torch.cuda.current_stream().query(), "the stream has to be behind still"
+    assert not used & {t.data_ptr() for t in got}
+    torch.cuda.synchronize()
+    assert opt.status(side) == (0, 0) and all(torch.equal(a, b) for a, b in zip(got, want))
+    # dropped while the current stream still reads them: not handed out again on their own stream
+    torch.cuda._sleep(200_000_000)
+    kept = [t * 2 for t in got]
+    used = {t.data_ptr() for t in got}
+    del got
+    with torch.cuda.stream(side):
+        new = [torch.full((opt.moment_elems,), 9.0, dtype=dtype, device="cuda") for _ in range(4)]
+    assert not torch.cuda.current_stream().query(), "the stream has to be behind still"
+    assert not used & {t.data_ptr() for t in new}
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(kept, doubled))
+
+
 # ---------------------------------------------------------------- refusals
 
 def test_binding_refuses(torch, bd):

@@ -216,3 +216,62 @@ def test_draws_are_uniform_and_independent():
             assert abs(x.mean()) * np.sqrt(len(x)) < 6
     assert not np.array_equal(oa.draws(1, 1, 0, i)[0], oa.draws(1, 1, 1, i)[0])
     assert not np.array_equal(oa.draws(1, 1, 0, i)[0], oa.draws(1 + (1 << 32), 1, 0, i)[0])
+
+
+# ---------------------------------------------------------------- the binding's streams
+
+class FakeMemory:
+    """What read_moments looks at in a tensor, and the stream that was current
+    when its memory was handed out."""
+
+    def __init__(self, n, dtype, on):
+        self.n, self.dtype, self.on, self.recorded = n, dtype, on, []
+
+    numel = lambda self: self.n
+    is_contiguous = lambda self: True
+    get_device = lambda self: 0
+    data_ptr = lambda self: 0x1000
+
+    def record_stream(self, stream):
+        self.recorded.append(stream)
+
+
+@pytest.mark.parametrize("given", ["", "m", "v"])
+def test_outputs_come_from_the_memory_of_the_stream_that_writes_them(monkeypatch, given):
+    torch = pytest.importorskip("torch")
+    import contextlib
+    import types
+    device = torch.device("cuda", 0)
+    ours, side = (types.SimpleNamespace(device=device, cuda_stream=h) for h in (7, 8))
+    current = [ours]
+
+    @contextlib.contextmanager
+    def stream(s):
+        current.append(current[-1] if s is None else s)
+        yield
+        current.pop()
+
+    fake = types.SimpleNamespace(stream=stream, current_stream=lambda device=None: current[-1])
+    monkeypatch.setattr(torch, "cuda", fake)
+    monkeypatch.setattr(torch, "empty", lambda n, dtype, device: FakeMemory(n, dtype, current[-1]))
+
+    def read(ctx, m, v, dtype, ws, ws_bytes, handle):
+        handles.append(handle)
+        return 0
+
+    opt = bd.AdamW.__new__(bd.AdamW)
+    opt.device, opt._index, opt.moment_elems = device, 0, 512
+    opt._cuda, opt._device, opt._current = fake, lambda: 0, lambda index: current[-1].cuda_stream
+    opt._ctx, opt._ws_at, opt._ws_bytes, opt._held, opt._streams = None, 0, 0, [], {7, 8}
+    opt._dtypes, opt._read = {torch.float32: bd.DTYPE_F32, torch.bfloat16: bd.DTYPE_BF16}, read
+    for s in (None, side):
+        handles = []
+        passed = {k: FakeMemory(512, torch.float32, ours) for k in given}
+        out = dict(zip("mv", opt.read_moments(stream=s, **passed)))
+        assert handles == [7 if s is None else 8] and current == [ours]
+        for k, t in out.items():
+            if k in passed:
+                assert t is passed[k] and (s is None or side in t.recorded)
+            else:  # another stream's memory would still be in that one's use
+                assert t.on is (ours if s is None else side)
+                assert s is None or ours in t.recorded
