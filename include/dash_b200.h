@@ -389,8 +389,8 @@ typedef struct shampoo_adamw shampoo_adamw;
  *    (1 + M/16) 2^(E-1), or M/16 for E = 0); scale byte i stands for
  *    2^(i - 127), the smallest power that brings the block's maximum within
  *    448 (m) or 31744 (r).  All bytes 0 are moments of zero.  r > 0 is never
- *    stored as 0.  Scale 255 marks a block that held a non-finite moment; the
- *    whole block reads back as not finite.
+ *    stored as 0.  Scale 255 marks a block that held a non-finite moment: the
+ *    whole block reads back as not finite, and so it stays.
  * An fp32 parameter may have a 16-bit `copy` of its new value written beside
  * it (rounded to nearest); a bf16 parameter is rounded stochastically. */
 typedef struct {
@@ -434,6 +434,9 @@ SHAMPOO_API int shampoo_adamw_bind(shampoo_adamw* ctx, int steps_taken, void* ws
  *   param -= lr lr_scale ( m_hat / (sqrt(v_hat) + adam_eps) + weight_decay param ),
  *   m_hat = m / (1 - beta1^t),  v_hat = v / (1 - beta2^t)
  * (the root of a v below fp32's normal range may come out smaller, down to 0).
+ * Where v overflows it is infinite, and the update only the decay's; in 8 bits
+ * v is then infinite for its whole block from the next step on.  An m that is
+ * not finite makes its parameter NaN, in 8 bits its block's at the next step.
  * 8-bit moments enter as the values they stand for; the update uses the new
  * moments before they are rounded.  Moments in 8 bits and bf16 parameters are
  * rounded stochastically: x lies between two neighbours of its format and

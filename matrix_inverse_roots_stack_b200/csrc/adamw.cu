@@ -59,7 +59,8 @@ __device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
 // product, and s + (v - s^2) y / 2 is off by the product of two errors before
 // it is rounded.  8-bit moments take this one: their codes then are those of
 // the correctly rounded root.  (The operand's floor keeps v = 0 at 0; below
-// the normal range the root comes out smaller.)
+// the normal range the root comes out smaller, and an infinite v's is NaN,
+// which the step sees to.)
 __device__ __forceinline__ float root(float v) {
   float r;
   asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
@@ -161,13 +162,14 @@ __device__ __forceinline__ unsigned m8_code(unsigned x, float y, unsigned u) {
 __device__ __forceinline__ unsigned v8_code(unsigned x, unsigned u) { return (x << kV8Shift) + u; }
 // r > 0 is never stored as 0: beside a nonzero first moment a vanished
 // second one would make the next update explode.  Four codes in one word:
-// whether one is 0, and the codes with 1 in its place where r > 0.
+// whether one is 0, and the codes with 1 in its place where r > 0, or
+// everywhere ('all': a block that is not finite reads back as infinite).
 __device__ __forceinline__ unsigned zero_bytes(unsigned w) { return (w - 0x01010101u) & ~w & 0x80808080u; }
-__device__ __forceinline__ unsigned v8_floor(unsigned w, const f32x2* r) {
+__device__ __forceinline__ unsigned v8_floor(unsigned w, const f32x2* r, bool all) {
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
     const float x = j & 1 ? high(r[j / 2]) : low(r[j / 2]);
-    if (x > 0.0f && !(w & (0xffu << (8 * j)))) w |= 1u << (8 * j);
+    if ((all || x > 0.0f) && !(w & (0xffu << (8 * j)))) w |= 1u << (8 * j);
   }
   return w;
 }
@@ -440,6 +442,31 @@ __device__ __forceinline__ bool step_block(const TileDesc& t, int pt, int gt, in
     rmax = kEight ? max_abs3(rmax, low(r[j]), high(r[j])) : max_abs3(rmax, low(v[j]), high(v[j]));
     zero = fma2(p[j], 0ull, zero);
   }
+  if (kEight && not_finite(rmax)) {
+    // v has overflowed, now or before: sqrt(v) is infinite, m / sqrt(v) is 0 and the update only the decay.  Rare, so
+    // the parameters are read again here; a select in root2, for every element, made the step of GPT-2's tables 111.2
+    // us instead of 110.1.
+    float y[8];
+    if (kAccess == kScalar) {
+      load8_strided(from, i0, left, pt, y);
+    } else {
+      if (kAccess == kStaged) load8_shared(stage, (at >> 3) + lane, pt, rp);
+      else load8(from, lane, pt, rp);
+      widen8(rp, pt, y);
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const float x = j & 1 ? high(r[j / 2]) : low(r[j / 2]), mj = j & 1 ? high(m[j / 2]) : low(m[j / 2]);
+      const float old = j & 1 ? high(p[j / 2]) : low(p[j / 2]);
+      y[j] = x != x && !not_finite(mj) ? fmaf(t.neg_lr, t.decay * y[j], y[j]) : old;
+    }
+    zero = 0ull;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      p[j] = pack2(y[2 * j], y[2 * j + 1]);
+      zero = fma2(p[j], 0ull, zero);
+    }
+  }
   const bool p_bad = low(zero) + high(zero) != 0.0f;
   const bool bad = p_bad || not_finite(max_abs3(0.0f, mmax, rmax));
 
@@ -508,8 +535,8 @@ __device__ __forceinline__ bool step_block(const TileDesc& t, int pt, int gt, in
     const uint2 am = make_uint2(top_bytes(a[0], a[1], a[2], a[3]), top_bytes(a[4], a[5], a[6], a[7]));
     uint2 bv = make_uint2(top_bytes(b[0], b[1], b[2], b[3]), top_bytes(b[4], b[5], b[6], b[7]));
     if (zero_bytes(bv.x) | zero_bytes(bv.y)) {
-      bv.x = v8_floor(bv.x, r);
-      bv.y = v8_floor(bv.y, r + 2);
+      bv.x = v8_floor(bv.x, r, not_finite(rmax));
+      bv.y = v8_floor(bv.y, r + 2, not_finite(rmax));
     }
     if (kAccess == kStaged) {
       if (lane == 0) most[at >> 8] = make_float2(mmax, rmax);
@@ -998,8 +1025,8 @@ __global__ void __launch_bounds__(kListThreads) load_moments_kernel(const AdamwT
       uint2 bv = make_uint2(top_bytes(cb[0], cb[1], cb[2], cb[3]), top_bytes(cb[4], cb[5], cb[6], cb[7]));
       if (zero_bytes(bv.x) | zero_bytes(bv.y)) {
         const f32x2 r2[4] = {pack2(r[0], r[1]), pack2(r[2], r[3]), pack2(r[4], r[5]), pack2(r[6], r[7])};
-        bv.x = v8_floor(bv.x, r2);
-        bv.y = v8_floor(bv.y, r2 + 2);
+        bv.x = v8_floor(bv.x, r2, not_finite(rmax));
+        bv.y = v8_floor(bv.y, r2 + 2, not_finite(rmax));
       }
       if (lane == 0) {
         t.m_scale[e0 >> 8] = mi.byte(mmax);

@@ -427,6 +427,52 @@ def test_non_finite_gradients_without_a_coefficient(torch, bd):
         guard.check()
 
 
+@pytest.mark.parametrize("bits", [32, 8])
+@pytest.mark.parametrize("param,grad", [("float32", "float32"), ("float32", "bfloat16"), ("bfloat16", "float32"),
+                                        ("bfloat16", "bfloat16")])
+@pytest.mark.parametrize("n,offset", [(1500, 0), (1500, 1), (4096 * 160 + 9, 0), (4096 * 160 + 9, 1)])
+def test_gradients_whose_square_overflows(torch, bd, bits, param, grad, n, offset):
+    # finite gradients, infinite second moments: sqrt(inf) = inf, m / inf = 0, and only the decay moves the parameter.
+    # In 8 bits v is infinite for the block from the next step on.  Short lists and long ones, which go through the ring
+    opt, guard, gen = make(torch, bd, [(n,)], bits, getattr(torch, param), getattr(torch, grad), None, offset, seed=9)
+    big = [3, 700, 702, 1499] if n < 4096 else [3, 700, 4096 * 100 + 255, 4096 * 160 - 1, n - 1]
+    over = np.zeros(n, bool)
+    over[big] = True
+    lr, decay = float(np.float32(1e-2)), float(np.float32(0.1))
+    frozen = over
+    for t in range(1, 4):
+        opt.grads[0].copy_(torch.randn(n, generator=gen))
+        if t == 1:
+            for i, x in zip(big, (1e21, -1e30, 6e20, -3e21, 2e25)):
+                opt.grads[0][i] = x
+        before = snapshot(opt)
+        opt.step(1e-2)
+        assert opt.status() == (bd.SHAMPOO_ENONFINITE, 1)
+        p0, got = before[0][0], f64(opt.params[0])
+        p = p0 - lr * decay * p0
+        e = 3 * H * (np.abs(p) + lr * decay * np.abs(p0))  # product, sum and last sum, each of them one rounding
+        if param == "float32":
+            assert np.all(np.abs(got - p)[frozen] <= e[frozen])
+        else:
+            dp = oa.draws(opt.hp.seed, t, 0, np.arange(n))[2]
+            lo, hi = (oa.on_grid(np.maximum(np.abs(p) + s * e, 0), oa.BF16_FORMAT, dp) for s in (-1, 1))
+            assert np.all(((lo <= np.abs(got)) & (np.abs(got) <= hi))[frozen])
+        assert np.isfinite(got).all()
+        other = [np.where(frozen, 0.0, x) for x in before[0]]  # the others as ever
+        if t == 1:
+            P, g, m, v = other
+            want, _, _ = oa.step(P, g, m, v, 1, opt.hp.beta1, opt.hp.beta2, opt.hp.adam_eps, lr, decay)
+            tol = lr * 30 * H + 1.01 * (H if param == "float32" else 2.0 ** -7) * np.abs(want)
+            assert np.all(np.abs(got - want)[~frozen] <= tol[~frozen])
+        if bits == 8:
+            frozen = np.repeat(np.add.reduceat(over, np.arange(0, n, 256)) > 0, 256)[:n]
+            assert np.array_equal(opt.v_scale[0].cpu().numpy() == 255, frozen[::256])
+            assert not bool((opt.m_scale[0] == 255).any())
+        m, v = (f64(opt.views(x)[0]) for x in opt.read_moments())
+        assert np.isfinite(m).all() and np.array_equal(v == np.inf, frozen) and not np.isnan(v).any()
+    guard.check()
+
+
 def test_bf16_parameters_stay_infinite_or_nan(torch, bd):
     P = [torch.tensor([float("inf"), -float("inf"), float("nan"), 1.0], dtype=torch.bfloat16, device="cuda")]
     G = [torch.zeros(4, device="cuda")]
@@ -532,6 +578,25 @@ def test_moments_of_extreme_size(torch, bd):
     opt.load_moments(m, v)
     assert opt.status() == (bd.SHAMPOO_ENONFINITE, 1)
     assert opt.m_scale[0].tolist()[1] == 255 and opt.v_scale[0].tolist()[2] == 255
+
+
+@pytest.mark.parametrize("offset", [0, 1])
+def test_infinite_second_moments_loaded_freeze_their_block(torch, bd, offset):
+    # the block reads back as infinite, zeros in it too, and its parameters have no update but the decay
+    opt, guard, gen = make(torch, bd, [(700,)], 8, torch.float32, torch.float32, None, offset, decay=0.5)
+    m, v = torch.zeros(768, device="cuda"), torch.zeros(768, device="cuda")
+    v[300] = float("inf")
+    opt.load_moments(m, v)
+    assert opt.status() == (bd.SHAMPOO_ENONFINITE, 1) and opt.v_scale[0].tolist() == [1, 255, 1]
+    assert torch.equal(opt.views(opt.read_moments()[1])[0] == float("inf"), torch.arange(700, device="cuda") // 256 == 1)
+    opt.grads[0].fill_(1.0)
+    p0 = f64(opt.params[0])
+    opt.step(0.125)
+    got = f64(opt.params[0])
+    want = p0 * (1 - 0.125 * 0.5)
+    assert np.all(np.abs(got - want)[256:512] <= 3 * H * np.abs(p0)[256:512])
+    assert np.all(np.abs(got - (want - 0.125))[np.r_[0:256, 512:700]] <= 0.125 * 30 * H + 1e-8)  # g / (|g| + eps)
+    guard.check()
 
 
 # ---------------------------------------------------------------- graphs and streams
