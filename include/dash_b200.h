@@ -300,9 +300,11 @@ SHAMPOO_API int shampoo_profile_read(double* out, int n);
 
 /* Test hook for the failure path (not part of the method): arms a one-shot
  * fault so that the next launch of a tensor-core product kernel (the GEMM,
- * or Newton-DB on resident factors of 128), or the next AdamW step if that
- * comes first, withholds its operand loads (an AdamW list of fewer tiles of 4096
- * elements than the device has SMs has none to withhold).  Its bounded waits then expire (about 2 s), the kernel sets
+ * or Newton-DB on resident factors of 128), or the next AdamW step that has
+ * any if that comes first, withholds its operand loads.  (A step has some
+ * where its list is of more tiles of 4096 elements than the device has SMs,
+ * and a whole one is in an aligned tensor; other steps leave the fault armed.)
+ * Its bounded waits then expire (about 2 s), the kernel sets
  * SHAMPOO_STATUS_TIMEOUT in the workspace status word, releases its tensor
  * memory and returns; the context stays usable.  The results of that call
  * are undefined. */

@@ -19,6 +19,7 @@ struct shampoo_adamw {
   AdamwHeader start{};         // header that bind uploads
   int bits = 32;               // of every tensor's moments, or 0
   int stage_bytes = 0;         // of a tile in shared memory, at most
+  bool stages = false;         // there are tiles that a step can fetch into shared memory
   int64_t blocks = 0, tiles = 0;
   size_t off_tensors = 0, total = 0;  // workspace
   const void* bound_ws = nullptr;
@@ -86,6 +87,7 @@ void add_tensor(shampoo_adamw* c, const shampoo_adamw_tensor& q, int index) {
   r.index = index;
   r.lr_scale = q.lr_scale;
   r.decay = q.weight_decay;
+  c->stages = c->stages || ((r.flags & dash::kFlagWide) && q.n >= dash::kTile);
   c->bits = c->tensors.empty() || c->bits == q.state_bits ? q.state_bits : 0;
   c->first_tile.push_back(r.first_tile);
   c->tensors.push_back(r);
@@ -224,7 +226,8 @@ int shampoo_adamw_step(shampoo_adamw* c, int step, float lr, const float* lr_dev
   a.eps = c->hp.adam_eps;
   a.seed_lo = static_cast<unsigned>(c->hp.seed);
   a.seed_hi = static_cast<unsigned>(c->hp.seed >> 32);
-  a.withhold = dash::take_load_fault() ? 1 : 0;
+  // only a step that has loads to withhold takes the fault
+  a.withhold = c->stages && c->tiles > c->launch.direct && dash::take_load_fault() ? 1 : 0;
   a.step = step;
   if (step > 0) {
     const StepConstants s = step_constants(c->hp, step);

@@ -890,6 +890,26 @@ def test_waits_for_tiles_are_bounded(torch, bd):
     assert bool(((p - 0.99).abs() <= 1e-6).all())
 
 
+def test_steps_without_loads_to_withhold_leave_the_fault_armed(torch, bd):
+    # the hook is for the next step that fetches tiles ahead: not one of few tiles, nor one whose tiles bulk copies
+    # cannot reach
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    one = lambda n, off=0: torch.ones(n + off, device="cuda")[off:]
+    short = bd.AdamW([one(4096 * sms)], [one(4096 * sms)])
+    odd = bd.AdamW([one(4096 * 2 * sms, 1)], [one(4096 * 2 * sms)])
+    small = bd.AdamW([one(4095) for _ in range(2 * sms)], [one(4095) for _ in range(2 * sms)])
+    long = bd.AdamW([one(4096 * (sms + 1))], [one(4096 * (sms + 1))])
+    assert bd.load().shampoo_debug_inject_timeout() == 0
+    for opt in (short, odd, small):
+        opt.step(1e-2)
+        assert opt.status() == (0, 0)
+        assert all(bool(((p - 0.99).abs() <= 1e-6).all()) for p in opt.params)
+    long.step(1e-2)
+    assert long.status() == (bd.SHAMPOO_ETIMEOUT, 2)
+    long.step(1e-2)
+    assert long.status() == (0, 0)
+
+
 @pytest.mark.parametrize("bits", [32, 8])
 def test_betas_of_zero(torch, bd, bits):
     hp = bd.make_adamw_hparams(beta1=0.0, beta2=0.0, seed=1)
