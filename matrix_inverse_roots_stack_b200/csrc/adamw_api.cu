@@ -23,6 +23,7 @@ struct shampoo_adamw {
   int64_t blocks = 0, tiles = 0;
   size_t off_tensors = 0, total = 0;  // workspace
   const void* bound_ws = nullptr;
+  dash::ListMemory all, written;  // the list's arrays, and those that calls write
   dash::AdamwLaunch launch{};
 };
 
@@ -116,8 +117,19 @@ int check_bound(const shampoo_adamw* c, const void* ws, size_t ws_bytes) {
   return ws == c->bound_ws ? SHAMPOO_OK : SHAMPOO_EINVAL;
 }
 
-// Flat moments; a list without elements has none.
+// Flat moments, and whether their memory is their own; a list without
+// elements has none.
 bool flat_ok(const shampoo_adamw* c, const void* p) { return c->blocks == 0 || (p && dash::aligned_to(p, 16)); }
+size_t flat_bytes(const shampoo_adamw* c, int dtype) {
+  return static_cast<size_t>(c->blocks) * dash::kQBlock * dash::dtype_bytes(dtype);
+}
+bool apart(const shampoo_adamw* c, const dash::ListMemory& from, const void* p, size_t bytes, const void* ws) {
+  return !from.meets(p, bytes) && !dash::share(p, bytes, ws, c->total);
+}
+// A rate or coefficient on the device.
+bool scalar_ok(const shampoo_adamw* c, const float* p, const void* ws) {
+  return !p || (dash::aligned_to(p, 4) && apart(c, c->written, p, sizeof(float), ws));
+}
 
 AdamwTable table(const shampoo_adamw* c, const void* ws) {
   const char* w = static_cast<const char*>(ws);
@@ -164,6 +176,8 @@ int shampoo_adamw_init(shampoo_adamw** out, const shampoo_adamw_tensor* tensors,
       delete c;
       return SHAMPOO_EINVAL;
     }
+    c->all = dash::ListMemory(ranges, false);
+    c->written = dash::ListMemory(ranges, true);
     for (int i = 0; i < n_tensors; ++i)
       if (tensors[i].n > 0) add_tensor(c, tensors[i], i);
     if (c->tensors.empty()) c->stage_bytes = dash::adamw_stage_bytes(false, SHAMPOO_DTYPE_F32, SHAMPOO_DTYPE_F32);
@@ -182,6 +196,7 @@ int shampoo_adamw_init(shampoo_adamw** out, const shampoo_adamw_tensor* tensors,
 int shampoo_adamw_bind(shampoo_adamw* c, int steps_taken, void* ws, size_t ws_bytes, void* stream) {
   if (!c || steps_taken < 0) return SHAMPOO_EINVAL;
   if (!ws || !dash::aligned_to(ws, 256) || ws_bytes < c->total) return SHAMPOO_EWORKSPACE;
+  if (c->all.meets(ws, c->total)) return SHAMPOO_EINVAL;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
   if (cudaStreamIsCapturing(st, &cap) != cudaSuccess) return SHAMPOO_ECUDA;
@@ -214,7 +229,7 @@ int shampoo_adamw_step(shampoo_adamw* c, int step, float lr, const float* lr_dev
                        size_t ws_bytes, void* stream) {
   const int rc = check_bound(c, ws, ws_bytes);
   if (rc) return rc;
-  if (step < 0 || (!lr_device && !std::isfinite(lr)) || !dash::aligned_to(lr_device, 4) || !dash::aligned_to(coef, 4))
+  if (step < 0 || (!lr_device && !std::isfinite(lr)) || !scalar_ok(c, lr_device, ws) || !scalar_ok(c, coef, ws))
     return SHAMPOO_EINVAL;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   dash::AdamwArgs a{};
@@ -251,7 +266,10 @@ int shampoo_adamw_load_moments(shampoo_adamw* c, const float* m, const float* v,
                                void* stream) {
   const int rc = check_bound(c, ws, ws_bytes);
   if (rc) return rc;
-  if (!flat_ok(c, m) || !flat_ok(c, v)) return SHAMPOO_EINVAL;
+  const size_t bytes = flat_bytes(c, SHAMPOO_DTYPE_F32);
+  if (!flat_ok(c, m) || !flat_ok(c, v) || !apart(c, c->written, m, bytes, ws) ||
+      !apart(c, c->written, v, bytes, ws))
+    return SHAMPOO_EINVAL;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (cudaMemsetAsync(ws, 0, sizeof(unsigned), st) != cudaSuccess) return SHAMPOO_ECUDA;
   if (c->blocks == 0) return SHAMPOO_OK;
@@ -264,6 +282,9 @@ int shampoo_adamw_read_moments(shampoo_adamw* c, void* m, void* v, int dtype, vo
   const int rc = check_bound(c, ws, ws_bytes);
   if (rc) return rc;
   if ((dtype != SHAMPOO_DTYPE_F32 && dtype != SHAMPOO_DTYPE_BF16) || !flat_ok(c, m) || !flat_ok(c, v))
+    return SHAMPOO_EINVAL;
+  const size_t bytes = flat_bytes(c, dtype);
+  if (dash::share(m, bytes, v, bytes) || !apart(c, c->all, m, bytes, ws) || !apart(c, c->all, v, bytes, ws))
     return SHAMPOO_EINVAL;
   if (c->blocks == 0) return SHAMPOO_OK;
   dash::launch_read_moments(table(c, ws), m, v, dtype, static_cast<cudaStream_t>(stream));

@@ -211,6 +211,7 @@ __global__ void __launch_bounds__(kListThreads) grad_clip_kernel(const GradChunk
 struct shampoo_grads {
   std::vector<dash::GradChunk> chunks;
   size_t off_partial = 0, total = 0;
+  dash::ListMemory memory;
   const void* bound_ws = nullptr;
   int shares = 0, rounds = 1, grid = 1;
 };
@@ -225,6 +226,7 @@ int norm_pass(shampoo_grads* c, float max_norm, float inv_scale, float* out, voi
     return SHAMPOO_EINVAL;
   if (!ws || ws_bytes < c->total) return SHAMPOO_EWORKSPACE;
   if (ws != c->bound_ws) return SHAMPOO_EINVAL;
+  if (c->memory.meets(out, 2 * sizeof(float)) || dash::share(out, 2 * sizeof(float), ws, c->total)) return SHAMPOO_EINVAL;
   char* w = static_cast<char*>(ws);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const auto* table = reinterpret_cast<const dash::GradChunk*>(w + dash::kHeaderBytes);
@@ -273,6 +275,7 @@ int shampoo_grads_init(shampoo_grads** out, const shampoo_grad* grads, int n_gra
       delete c;
       return SHAMPOO_EINVAL;
     }
+    c->memory = dash::ListMemory(ranges, false);
   } catch (...) {
     delete c;
     return SHAMPOO_EINVAL;
@@ -288,6 +291,7 @@ int shampoo_grads_init(shampoo_grads** out, const shampoo_grad* grads, int n_gra
 int shampoo_grads_bind(shampoo_grads* c, void* ws, size_t ws_bytes, void* stream) {
   if (!c) return SHAMPOO_EINVAL;
   if (!ws || !dash::aligned_to(ws, 256) || ws_bytes < c->total) return SHAMPOO_EWORKSPACE;
+  if (c->memory.meets(ws, c->total)) return SHAMPOO_EINVAL;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
   if (cudaStreamIsCapturing(st, &cap) != cudaSuccess) return SHAMPOO_ECUDA;

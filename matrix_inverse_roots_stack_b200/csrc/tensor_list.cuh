@@ -48,6 +48,33 @@ inline void add_range(std::vector<ByteRange>& r, const void* p, size_t bytes, bo
   const uintptr_t lo = reinterpret_cast<uintptr_t>(p);
   if (bytes) r.push_back({lo, lo + bytes, written});
 }
+inline bool share(const void* p, size_t p_bytes, const void* q, size_t q_bytes) {
+  const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
+  return p_bytes && q_bytes && a < b + q_bytes && b < a + p_bytes;
+}
+
+// A list's memory, kept for the buffers that later calls pass: disjoint
+// ranges in order, made of those that ranges_clash has sorted.
+class ListMemory {
+ public:
+  ListMemory() = default;
+  ListMemory(const std::vector<ByteRange>& sorted, bool written_only) {
+    for (const ByteRange& x : sorted) {
+      if (written_only && !x.written) continue;
+      if (ends_.empty() || x.lo > ends_.back().second) ends_.emplace_back(x.lo, x.hi);
+      else ends_.back().second = std::max(ends_.back().second, x.hi);
+    }
+  }
+  bool meets(const void* p, size_t bytes) const {
+    const uintptr_t lo = reinterpret_cast<uintptr_t>(p);
+    const auto behind = std::lower_bound(ends_.begin(), ends_.end(), lo + bytes,
+                                         [](const auto& x, uintptr_t at) { return x.first < at; });
+    return bytes && behind != ends_.begin() && (behind - 1)->second > lo;
+  }
+
+ private:
+  std::vector<std::pair<uintptr_t, uintptr_t>> ends_;
+};
 
 // ------------------------------------------------------------ device side
 

@@ -799,6 +799,41 @@ def test_binding_refuses(torch, bd):
     assert opt.steps_taken() == 0 and not bool(p.any())
 
 
+def test_buffers_that_share_memory_are_refused(torch, bd):
+    n = 512
+    z = lambda k=n, dtype=torch.float32: torch.zeros(k, dtype=dtype, device="cuda")
+    p, g, big = z(), z(), z(2 * n + 8)
+    for bits in (32, 8):
+        opt, clip = bd.AdamW([p], [g], state_bits=bits), bd.GradClip([g])
+        own = [opt.m[0], opt.v[0]] if bits == 32 else []
+        ok = big[:n], big[n:2 * n]
+        opt.read_moments(m=ok[0], v=ok[1])
+        opt.load_moments(*ok)
+        opt.load_moments(ok[0], ok[0])  # both are only read
+        opt.load_moments(g, ok[0])
+        for m, v in [(ok[0], ok[0]), (big[4:n + 4], ok[0]), (ok[1], big[n + 8:]), (p, ok[0]), (ok[0], p), (g, ok[0]),
+                     (ok[1], g)] + [(t, ok[0]) for t in own] + [(ok[0], t) for t in own]:
+            with pytest.raises(bd.ShampooError):
+                opt.read_moments(m=m, v=v)
+        half = big.view(torch.bfloat16)
+        opt.read_moments(m=half[:n], v=half[n:2 * n])
+        with pytest.raises(bd.ShampooError):
+            opt.read_moments(m=half[:n], v=half[n - 8:2 * n - 8])
+        for m, v in [(p, ok[0]), (ok[0], p)] + [(t, ok[0]) for t in own] + [(ok[0], t) for t in own]:
+            with pytest.raises(bd.ShampooError):
+                opt.load_moments(m, v)
+        for s in [p[7:8]] + [t[:1] for t in own]:
+            for kw in (dict(lr=s), dict(coef=s)):
+                with pytest.raises(bd.ShampooError):
+                    opt.step(**kw)
+        opt.step(g[3:4], coef=big[:1])  # a gradient is only read: lr 0
+        lib, stream = bd.load(), torch.cuda.current_stream().cuda_stream
+        for fn in (lib.shampoo_grad_norm, lib.shampoo_grad_clip):
+            for at in (g.data_ptr(), g.data_ptr() + 4 * n - 4, g.data_ptr() - 4, clip.ws.data_ptr() + 8):
+                assert fn(clip._ctx, 1.0, 1.0, at, clip.ws.data_ptr(), clip.ws.numel(), stream) == bd.SHAMPOO_EINVAL
+        assert opt.status() == (0, 0) and clip.norm().tolist() == [0.0, 1.0] and not bool(p.any())
+
+
 # ---------------------------------------------------------------- bits
 
 @pytest.mark.parametrize("bits", [32, 8])

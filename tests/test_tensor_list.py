@@ -175,6 +175,28 @@ def test_binding_refuses_lists_without_cuda_tensors(lib, make):
         make(pytest.importorskip("torch"))
 
 
+def test_workspace_shares_no_memory_with_the_list(lib):
+    # two tensors with a hole between them; a workspace that reaches into either, or lies around one, is refused
+    # before anything is uploaded, one in the hole or behind goes on to the device
+    gpu = pytest.importorskip("torch").cuda.is_available()
+    rc, grads, need = grads_init(lib, [(100, 0x100000, bd.DTYPE_F32), (100, 0x300000, bd.DTYPE_F32)])
+    rc2, adamw, need2, _ = adamw_init(lib, [tensor(0x100000), tensor(0x300000, grad=0x110000)])
+    assert rc == 0 and rc2 == 0
+    for bind, ctx, n in ((lambda *a: lib.shampoo_grads_bind(*a, None), grads, need),
+                         (lambda c, *a: lib.shampoo_adamw_bind(c, 0, *a, None), adamw, need2)):
+        low = -(-n // 256) * 256
+        for at, ok in ((0x100000, False), (0x300000, False), (0x300100, False), (0x300000 - low, True),
+                       (0x300000 - low + 256, n <= low - 256), (0x100000 - low, True), (0x100000 - 256, n <= 256),
+                       (0x800000, True), (0x200000, True)):
+            if not (ok and gpu):  # no made-up address goes to a device
+                assert (bind(ctx, ctypes.c_void_p(at), n) != bd.SHAMPOO_EINVAL) == ok, hex(at)
+    # arrays of which others are read only
+    for at in (0x110000, 0x120000, 0x130f00, 0x320000):
+        assert lib.shampoo_adamw_bind(adamw, 0, ctypes.c_void_p(at), need2, None) == bd.SHAMPOO_EINVAL
+    lib.shampoo_grads_destroy(grads)
+    lib.shampoo_adamw_destroy(adamw)
+
+
 # ---------------------------------------------------------------- the oracle's formats
 
 @pytest.mark.parametrize("fmt", [oa.M_FORMAT, oa.V_FORMAT])
