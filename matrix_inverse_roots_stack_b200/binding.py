@@ -623,19 +623,21 @@ class AdamW(_TensorList):
         return out
 
     def read_moments(self, dtype=None, m=None, v=None, stream=None):
-        """Both moments as flat tensors (see :meth:`views`) of fp32 (default)
-        or bf16, into m and v where given.  Those that are not given are made
+        """Both moments as flat tensors (see :meth:`views`) of fp32 or bf16
+        (default: the type of the one that is given, or fp32), into m and v
+        where given.  Those that are not given are made
         on `stream`: other streams wait for it before they use them."""
         if m is None or v is None:
             import torch
-            made = []
+            made, given = [], m if v is None else v
+            of = dtype or (torch.float32 if given is None else given.dtype)
             # not from the current stream's memory: what was freed there may be in its queued work's use still
             with torch.cuda.stream(stream):
                 if m is None:
-                    m = torch.empty(self.moment_elems, dtype=dtype or torch.float32, device=self.device)
+                    m = torch.empty(self.moment_elems, dtype=of, device=self.device)
                     made.append(m)
                 if v is None:
-                    v = torch.empty(self.moment_elems, dtype=m.dtype, device=self.device)
+                    v = torch.empty(self.moment_elems, dtype=of, device=self.device)
                     made.append(v)
             if stream is not None:  # the caller's stream uses them next
                 for t in made:

@@ -297,3 +297,42 @@ def test_outputs_come_from_the_memory_of_the_stream_that_writes_them(monkeypatch
             else:  # another stream's memory would still be in that one's use
                 assert t.on is (ours if s is None else side)
                 assert s is None or ours in t.recorded
+
+
+def fake_list(torch, elems=512):
+    """An AdamW object whose read calls go nowhere."""
+    import contextlib
+    import types
+    cuda = types.SimpleNamespace(stream=lambda s: contextlib.nullcontext(), current_stream=lambda device=None: None)
+    opt = bd.AdamW.__new__(bd.AdamW)
+    opt.device, opt._index, opt.moment_elems, opt._ctx = torch.device("cuda", 0), 0, elems, None
+    opt._cuda, opt._device, opt._current, opt._streams = cuda, lambda: 0, lambda index: 7, {7}
+    opt._ws_at, opt._ws_bytes, opt._held = 0, 0, []
+    opt._dtypes = {torch.float32: bd.DTYPE_F32, torch.bfloat16: bd.DTYPE_BF16}
+    opt.calls = []
+
+    def call(*args):
+        opt.calls.append(args)
+        return 0
+
+    opt._read = opt._step = call
+    return opt, cuda
+
+
+@pytest.mark.parametrize("given", ["m", "v", "mv", ""])
+@pytest.mark.parametrize("kind", ["float32", "bfloat16"])
+def test_the_moment_that_is_not_given_takes_the_type_of_the_other(monkeypatch, given, kind):
+    torch = pytest.importorskip("torch")
+    opt, cuda = fake_list(torch)
+    monkeypatch.setattr(torch, "cuda", cuda)
+    monkeypatch.setattr(torch, "empty", lambda n, dtype, device: FakeMemory(n, dtype, None))
+    kind = getattr(torch, kind)
+    for dtype in (None, kind):
+        passed = {k: FakeMemory(512, kind, None) for k in given}
+        out = opt.read_moments(dtype, **passed)
+        want = kind if given or dtype is not None else torch.float32
+        assert [t.dtype for t in out] == [want, want] and opt.calls[-1][3] == opt._dtypes[want]
+    if given:
+        other = torch.float32 if kind is torch.bfloat16 else torch.bfloat16
+        with pytest.raises(ValueError):
+            opt.read_moments(other, **{k: FakeMemory(512, kind, None) for k in given})
