@@ -30,6 +30,7 @@ DTYPE_F32 = 0
 DTYPE_BF16 = 1
 DTYPE_F16 = 2
 QBLOCK = 256  # elements that share a scale in 8-bit moments
+MAX_STEP = 0x7fffffff  # step numbers are C ints, which ctypes cuts to their low 32 bits
 
 
 class ShampooError(RuntimeError):
@@ -525,6 +526,8 @@ class AdamW(_TensorList):
         self.copies = each(copies, "copies")
         if any(b not in (8, 32) for b in self.state_bits):
             raise ValueError("state_bits must be 8 or 32")
+        if not -MAX_STEP <= steps_taken <= MAX_STEP:  # the library refuses negative ones
+            raise ValueError(f"steps_taken {steps_taken} is not a 32-bit number")
         if len(self.grads) != n:
             raise ValueError(f"{len(self.grads)} gradients for {n} parameters")
         _check_list(self.params, "params", (f32, bf16), dev)
@@ -593,6 +596,8 @@ class AdamW(_TensorList):
                 lr = float(lr)
         if coef is not None:
             coef_at = self._scalar(coef, "coef")
+        if not -MAX_STEP <= step <= MAX_STEP:  # the library refuses negative ones
+            raise ValueError(f"step {step} is not a 32-bit number")
         self._run(self._step, self._ctx, step, lr, lr_at, coef_at, self._ws_at, self._ws_bytes,
                   self._on(stream, held, coef))
 

@@ -336,3 +336,22 @@ def test_the_moment_that_is_not_given_takes_the_type_of_the_other(monkeypatch, g
         other = torch.float32 if kind is torch.bfloat16 else torch.bfloat16
         with pytest.raises(ValueError):
             opt.read_moments(other, **{k: FakeMemory(512, kind, None) for k in given})
+
+
+@pytest.mark.parametrize("step", [1 << 31, 1 << 32, (1 << 32) + 5, -(1 << 32), -(1 << 32) + 3])
+def test_step_numbers_are_not_cut_to_32_bits(step):
+    # 2^32 would continue the counter, 2^32 + 5 be step 5
+    torch = pytest.importorskip("torch")
+    opt, _ = fake_list(torch)
+    opt.step(1e-3, step=(1 << 31) - 1)
+    assert opt.calls[-1][1] == (1 << 31) - 1
+    with pytest.raises(ValueError, match="32-bit"):
+        opt.step(1e-3, step=step)
+    assert len(opt.calls) == 1
+
+    class Param(FakeMemory):
+        device, shape, is_contiguous = torch.device("cuda", 0), (512,), lambda self: True
+
+    p, g = Param(512, torch.float32, None), Param(512, torch.float32, None)
+    with pytest.raises(ValueError, match="steps_taken"):
+        bd.AdamW([p], [g], steps_taken=step)
