@@ -372,10 +372,12 @@ def _dtype_code(t):
 
 
 def _check_list(tensors, what, dtypes, device, like=None):
-    """Contiguous CUDA tensors of one device and of the given types; `like`:
-    tensors whose shapes they have."""
+    """Contiguous CUDA tensors (or None entries) of one device and of the given
+    types; `like`: tensors whose shapes they have."""
     index = device.index
     for i, t in enumerate(tensors):
+        if t is None:
+            continue
         if t.dtype not in dtypes or t.get_device() != index or not t.is_contiguous():
             raise ValueError(f"{what}[{i}] must be a contiguous tensor on {device} of type "
                              f"{' or '.join(str(d) for d in dtypes)}")
@@ -549,7 +551,7 @@ class AdamW(_TensorList):
                     raise ValueError(f"{what}[{i}] has {t.numel()} elements, not {numel}")
                 elif t.dtype != dtype:
                     raise ValueError(f"{what}[{i}] must be of type {dtype}")
-            _check_list([t for t in out if t is not None], what, (f32, torch.uint8), dev)
+            _check_list(out, what, (f32, torch.uint8), dev)
             return out
 
         codes = [torch.uint8 if e else f32 for e in eight]
@@ -558,10 +560,9 @@ class AdamW(_TensorList):
         self.m, self.v = state(m, "m", codes, sizes), state(v, "v", codes, sizes)
         self.m_scale = state(m_scale, "m_scale", bytes_, blocks)
         self.v_scale = state(v_scale, "v_scale", bytes_, blocks)
-        given = [(i, c) for i, c in enumerate(self.copies) if c is not None]
-        if any(self.params[i].dtype != f32 for i, _ in given):
+        if any(c is not None and p.dtype != f32 for p, c in zip(self.params, self.copies)):
             raise ValueError("copies are for fp32 parameters only")
-        _check_list([c for _, c in given], "copies", (bf16, f16), dev, [self.params[i] for i, _ in given])
+        _check_list(self.copies, "copies", (bf16, f16), dev, self.params)
         code = {f32: DTYPE_F32, bf16: DTYPE_BF16, f16: DTYPE_F16}
         at = lambda t: None if t is None else t.data_ptr()
         arr = (AdamwTensor * n)(*[

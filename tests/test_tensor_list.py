@@ -355,3 +355,27 @@ def test_step_numbers_are_not_cut_to_32_bits(step):
     p, g = Param(512, torch.float32, None), Param(512, torch.float32, None)
     with pytest.raises(ValueError, match="steps_taken"):
         bd.AdamW([p], [g], steps_taken=step)
+
+
+def test_a_refused_tensor_is_named_by_its_place_in_the_list():
+    torch = pytest.importorskip("torch")
+
+    class Tensor(FakeMemory):
+        device = torch.device("cuda", 0)
+
+        def __init__(self, shape=(512,), dtype=torch.float32):
+            super().__init__(512, dtype, None)
+            self.shape = shape
+
+    lists = dict(params=[Tensor() for _ in range(3)], grads=[Tensor() for _ in range(3)], m=[Tensor() for _ in range(3)])
+    with pytest.raises(ValueError, match=r"copies\[2\] must be"):
+        bd.AdamW(**lists, v=lists["m"], copies=[None, None, Tensor()])
+    with pytest.raises(ValueError, match=r"copies\[2\] has shape"):
+        bd.AdamW(**lists, v=lists["m"], copies=[Tensor(dtype=torch.bfloat16), None, Tensor((2, 256), torch.float16)])
+    eight = [Tensor(), Tensor(dtype=torch.uint8), Tensor(dtype=torch.uint8)]
+    bad = Tensor((2,), torch.uint8)
+    bad.n, bad.is_contiguous = 2, lambda: False
+    with pytest.raises(ValueError, match=r"m_scale\[2\] must be"):
+        good = Tensor((2,), torch.uint8)
+        good.n = 2
+        bd.AdamW(lists["params"], lists["grads"], m=eight, v=eight, m_scale=[None, good, bad], state_bits=[32, 8, 8])
