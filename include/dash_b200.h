@@ -368,8 +368,9 @@ SHAMPOO_API int shampoo_grads_bind(shampoo_grads* ctx, void* ws, size_t ws_bytes
  * that unscales and clips a gradient (device, 2 floats).  Sums are formed in
  * fp64 in a fixed order, so equal gradients give equal bits.  An element that
  * is not finite makes norm not finite and coef NaN and sets
- * SHAMPOO_STATUS_NONFINITE.  max_norm > 0 (infinity: no clipping), inv_scale
- * > 0 and finite (1 / loss scale). */
+ * SHAMPOO_STATUS_NONFINITE.  (The norm of finite elements may still round to
+ * infinity in fp32; coef is formed from the fp64 norm.)  max_norm > 0
+ * (infinity: no clipping), inv_scale > 0 and finite (1 / loss scale). */
 SHAMPOO_API int shampoo_grad_norm(shampoo_grads* ctx, float max_norm, float inv_scale, float* out, void* ws,
                                   size_t ws_bytes, void* stream);
 
@@ -455,7 +456,7 @@ SHAMPOO_API int shampoo_adamw_bind(shampoo_adamw* ctx, int steps_taken, void* ws
  * float, or NULL: 1) is shampoo_grad_norm's out + 1.  Where coef is not
  * finite the step is not taken: nothing is written, the counter stays, and
  * SHAMPOO_STATUS_NONFINITE is set.  That bit is also set when a moment or
- * parameter becomes non-finite. */
+ * parameter, as computed in fp32, is not finite. */
 SHAMPOO_API int shampoo_adamw_step(shampoo_adamw* ctx, int step, float lr, const float* lr_device, const float* coef,
                                    void* ws, size_t ws_bytes, void* stream);
 

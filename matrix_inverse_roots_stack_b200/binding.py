@@ -452,8 +452,9 @@ class GradClip(_TensorList):
     """Global norm and clipping of a list of CUDA gradients (fp32, bf16 or
     fp16, any shapes).  The gradients' addresses are fixed here, their values
     are read at every call.  Results stay on the device, in :attr:`out`:
-    [norm, coef], with coef = inv_scale min(1, max_norm / norm), NaN where the
-    norm is not finite."""
+    [norm, coef], with coef = inv_scale min(1, max_norm / norm), NaN where a
+    gradient is not finite.  (The norm of finite gradients that lies beyond
+    fp32 is infinite there, and coef finite all the same.)"""
 
     _destroy = "shampoo_grads_destroy"
 

@@ -688,7 +688,7 @@ __device__ __forceinline__ void write_scale(uint8_t* to, float2 most) {
 // A long list's tiles, dealt to the grid's blocks: share p < 'whole' is kDeal
 // tiles, a grid's width apart, so that blocks that run side by side read side
 // by side (kDeal tiles in a row, all blocks a multiple of that apart, cost
-// 8%); the last one or two grids of shares are single tiles.
+// 8%); the last four to eight grids' width of tiles are shares of one tile.
 struct Deal {
   int grid, whole, tile, left;  // tile: the current one; left: tiles behind it in its share
   __device__ __forceinline__ Deal(int n_tiles, int grid) : grid(grid), whole((n_tiles / (kDeal * grid) - 1) * grid) {}

@@ -47,7 +47,7 @@ struct AdamwHeader {
   unsigned status;
   unsigned ticket;
   unsigned bad;          // status bits of the running step
-  unsigned next;         // tiles taken in the running step, beyond the first of each block
+  unsigned next;         // shares taken in the running step, beyond the first of each block
   int t;                 // last step taken
   double pow1, pow2;     // beta1^t, beta2^t
   float d1, d0;          // for step t + 1, see AdamwArgs

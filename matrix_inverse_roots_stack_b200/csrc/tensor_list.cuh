@@ -1,6 +1,6 @@
 // Shared pieces of the kernels that work on a list of tensors in one launch
-// (adamw.cu, grad_norm.cu): element types, chunk tables, 8-element vector
-// accesses, and the host checks of a list.
+// (adamw.cu, grad_norm.cu): element types, 8-element vector accesses, and the
+// host checks of a list's memory.
 #pragma once
 
 #include <cstddef>
@@ -191,11 +191,7 @@ __device__ __forceinline__ void load8_strided(const void* base, int i, int n, in
   }
 }
 
-// Scalar path: element i of a buffer with no more than its type's alignment.
-__device__ __forceinline__ float load1(const void* base, int i, int dtype) {
-  if (dtype == SHAMPOO_DTYPE_F32) return static_cast<const float*>(base)[i];
-  return widen(static_cast<const unsigned short*>(base)[i], dtype);
-}
+// Element i of a buffer with no more than its type's alignment.
 __device__ __forceinline__ void store1(void* base, int i, int dtype, float x) {
   if (dtype == SHAMPOO_DTYPE_F32) static_cast<float*>(base)[i] = x;
   else static_cast<unsigned short*>(base)[i] = narrow(x, dtype);
