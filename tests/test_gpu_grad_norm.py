@@ -79,6 +79,42 @@ def test_norm_and_clip(torch, bd, sizes, dtype, offset):
             assert bool((raw[:offset] == 3).all()) and bool((raw[offset + g.numel():] == 3).all())
 
 
+@pytest.mark.parametrize("chunks_an_sm", [1, 3, 5, 7, 10, 14, 20, 30, 50, 100, 170])
+def test_long_lists(torch, bd, chunks_an_sm):
+    # chunks of 32 KB, from one an SM to more than 16 for each block that the device holds (two to eight an SM): one
+    # share a block, shares from the counter, of one chunk and of several, the last group short.  All types and odd
+    # ends, some tensors off 16 bytes.  Equal bits of every share's sum, which the workspace keeps, whatever else the
+    # device is doing
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    n = sms * chunks_an_sm * 8192 // 4  # fp32 elements of a quarter of the list
+    gen = torch.Generator("cuda").manual_seed(chunks_an_sm)
+    grads = []
+    for dtype, size, offset in ((torch.float32, n + 5, 0), (torch.bfloat16, 2 * n - 3, 0), (torch.float16, 2 * n + 1, 0),
+                                (torch.bfloat16, n, 1), (torch.float32, n // 2 + 77, 1)):
+        raw = torch.empty(size + offset, dtype=dtype, device="cuda")
+        raw.normal_(generator=gen)
+        grads.append(raw[offset:])
+    want = math.sqrt(math.fsum(float(g.double().square().sum()) for g in grads))
+    clip = bd.GradClip(grads)
+    norm = clip.norm(want / 2)[0].item()
+    assert abs(norm - want) <= 1.01 * H * want and clip.status() == (0, 0)
+    kept, out = clip.ws.clone(), clip.out.clone()
+    side, busy = torch.cuda.Stream(), torch.empty(1 << 24, device="cuda")
+    torch.cuda.synchronize()
+    for k in range(20):
+        with torch.cuda.stream(side):
+            for _ in range(k % 4):
+                busy.normal_()
+        clip.norm(want / 2)
+        assert torch.equal(clip.ws, kept) and torch.equal(clip.out, out)
+    torch.cuda.synchronize()
+    if chunks_an_sm in (3, 20):
+        before = [g.clone() for g in grads]
+        coef = clip.clip(want / 2)[1]
+        for g, b in zip(grads, before):  # the product in fp32, rounded to the type
+            assert torch.equal(g, (b.float() * coef).to(g.dtype))
+
+
 @pytest.mark.parametrize("value", [1e-38, 1e-30, 1e25, 3e38])
 def test_extreme_values(torch, bd, value):
     g = torch.full((5000,), value, device="cuda")
