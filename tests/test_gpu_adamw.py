@@ -901,6 +901,61 @@ def test_long_lists_are_dealt_out_completely(torch, bd):
             assert bool(((opt.views(v)[i].double() / (g * g * (1 - b2 * b2)) - 1).abs() < 1e-5).all())
 
 
+def test_dealt_out_tensors_have_the_bits_of_a_list_of_their_own(torch, bd):
+    # each tensor of a dealt-out list against a list whose other tensors are empty (the draws go by the place in the
+    # list), which is short enough for tiles in turn or for no ring at all; both widths and types, other alignments
+    gen = torch.Generator("cuda").manual_seed(14)
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    sizes = [4096 * 4 * sms, 4096 * 9 * sms + 17, 5, 4096, 4095, 4096 * 3 * sms, 100001] + [4096 * 3 + 1] * 20
+    assert sum(-(-n // 4096) for n in sizes) >= 16 * sms  # dealt out
+    spec = []
+    for i, n in enumerate(sizes):
+        at, bits = (1 if i % 5 == 4 else 0), (32 if i % 3 == 0 else 8)
+        param = torch.bfloat16 if i % 4 == 1 else torch.float32
+        spec.append((n, at, bits, torch.randn(n, generator=gen, device="cuda").to(param),
+                     torch.randn(n, generator=gen, device="cuda")))
+
+    def made(chosen):
+        P, G, M, V = [], [], [], []
+        for i, (n, at, bits, p, g) in enumerate(spec):
+            n = n if chosen is None or i == chosen else 0
+            code = torch.uint8 if bits == 8 else torch.float32
+            for out, x in ((P, p), (G, g)):
+                raw = torch.empty(n + at, dtype=x.dtype, device="cuda")
+                raw[at:].copy_(x[:n])
+                out.append(raw[at:])
+            for out in (M, V):
+                out.append(torch.zeros(n + at, dtype=code, device="cuda")[at:])
+        opt = bd.AdamW(P, G, state_bits=[s[2] for s in spec], m=M, v=V, weight_decay=0.1)
+        for _ in range(3):
+            opt.step(1e-2)
+        assert opt.status() == (0, 0) and opt.steps_taken() == 3
+        return opt
+
+    whole = made(None)
+    for i in range(len(spec)):
+        one = made(i)
+        for a, b in zip((whole.params, whole.m, whole.v, whole.m_scale, whole.v_scale),
+                        (one.params, one.m, one.v, one.m_scale, one.v_scale)):
+            assert a[i] is None and b[i] is None or torch.equal(a[i], b[i]), i
+
+
+def test_borders_of_tiles_and_shares(torch, bd):
+    # a dealt-out list of one tensor against the oracle where one tile, or one share, ends and another begins: blocks
+    # take shares of four tiles, a grid's width apart, and single tiles from the border on
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    tiles = 41 * sms + 3
+    n = 4096 * tiles + 1003
+    single = 4 * ((tiles + 1) // (4 * sms) - 1) * sms
+    P = [torch.full((n,), 1.0, dtype=torch.bfloat16, device="cuda")]
+    G = [torch.empty(n, dtype=torch.bfloat16, device="cuda").normal_(generator=torch.Generator("cuda").manual_seed(21))]
+    opt = bd.AdamW(P, G, state_bits=8, weight_decay=0.1)
+    opt.step(1e-2)
+    assert opt.status() == (0, 0)
+    ends = [1, sms, 4 * sms, 5 * sms, single - sms, single - 1, single, single + 1, single + sms, tiles - 1, tiles]
+    check_slices(torch, opt, [(0, 512)] + [(4096 * t - 256, min(4096 * t + 256, n)) for t in ends] + [(n - n % 256, n)])
+
+
 def test_counter_goes_on_from_a_late_step(torch, bd):
     p, g = torch.ones(1, device="cuda"), torch.ones(1, device="cuda")
     opt = bd.AdamW([p], [g], steps_taken=10 ** 6)

@@ -379,3 +379,22 @@ def test_a_refused_tensor_is_named_by_its_place_in_the_list():
         good = Tensor((2,), torch.uint8)
         good.n = 2
         bd.AdamW(lists["params"], lists["grads"], m=eight, v=eight, m_scale=[None, good, bad], state_bits=[32, 8, 8])
+
+
+def test_the_longest_tensors(lib):
+    # addresses are not touched; a gradient list describes 2^38 elements in chunks, 256 MB on the host
+    rc, ctx, _ = grads_init(lib, [(1 << 38, 1 << 40, bd.DTYPE_BF16)])
+    assert rc == bd.SHAMPOO_OK
+    lib.shampoo_grads_destroy(ctx)
+    assert grads_init(lib, [((1 << 38) + 1, 1 << 40, bd.DTYPE_BF16)])[0] == bd.SHAMPOO_EINVAL
+    at = dict(param=1 << 40, grad=2 << 40, m=3 << 40, v=4 << 40)
+    for extra in ({}, dict(state_bits=8, m_scale=5 << 40, v_scale=6 << 40)):
+        rc, ctx, _, elems = adamw_init(lib, [tensor(n=1 << 38, **at, **extra)])
+        assert rc == bd.SHAMPOO_OK and elems == 1 << 38
+        lib.shampoo_adamw_destroy(ctx)
+        more = {k: v + (1 << 43) for k, v in {**at, **extra}.items() if k != "state_bits"}
+        if extra:
+            more["state_bits"] = 8
+        for rows in ([tensor(n=(1 << 38) + 1, **at, **extra)],
+                     [tensor(n=1 << 38, **at, **extra), tensor(n=1 << 38, **more)]):
+            assert adamw_init(lib, rows)[0] == bd.SHAMPOO_EINVAL  # too long, or the list is
