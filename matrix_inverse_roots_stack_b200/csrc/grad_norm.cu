@@ -36,7 +36,9 @@ constexpr size_t kHeaderBytes = 256;
 constexpr int kChunkBytes = 32768;
 __host__ __device__ constexpr int chunk_elems(int dtype) { return kChunkBytes / (dtype == SHAMPOO_DTYPE_F32 ? 4 : 2); }
 constexpr int kLoads = kChunkBytes / (kListThreads * 16);  // 16-byte pieces of a thread
-constexpr int kTurns = 8;  // shares for each resident block in a long list, or up to twice that
+// Shares for each resident block in a long list, or up to twice that.  With 2, 4, 8, 16 and 32 of them 129 chunks a
+// block take 345, 343, 341, 345 and 346 us (fp32) and 16 chunks a block 51.4, 53, 52, 56 and 58 us (bf16).
+constexpr int kTurns = 8;
 
 __device__ __forceinline__ void add_squares(const float* x, double* acc) {
 #pragma unroll
@@ -301,8 +303,10 @@ int shampoo_grads_bind(shampoo_grads* c, void* ws, size_t ws_bytes, void* stream
   if (blocks < 0) return SHAMPOO_ECUDA;
   const int n = static_cast<int>(c->chunks.size());
   c->grid = std::max(1, std::min({n, blocks, kMaxShares / (2 * dash::kTurns)}));
-  // A list of under four chunks a block is one share a block: 12.6M fp32 elements take 14.6 us so, 15.9 taken chunk
-  // by chunk; at eight a block (39.4M) it is 36.5 and 31.5.
+  // A list of under four chunks a block is one share a block, a longer one shares from the counter.  The two in us, in
+  // a graph, by chunks a block: 2.6: 12.8 and 13.9; 4.25: 17.5 and 19.4; 8.1: 27.3 and 29.6; 16: 48.5 and 50.2; 32:
+  // 90.0 and 91.6; 129: 343.6 and 341 (all fp32), and in fp16, where the SMs drift apart most, 395 and 364.  So one
+  // share is ahead up to some 30 chunks a block already, by 2 to 10%.
   c->rounds = n < 4 * c->grid ? (n + c->grid - 1) / c->grid : std::max(1, n / (dash::kTurns * c->grid));
   // whole groups of grid x rounds chunks, the last one short
   const int group = c->grid * std::max(1, c->rounds);
