@@ -305,7 +305,7 @@ int shampoo_grads_bind(shampoo_grads* c, void* ws, size_t ws_bytes, void* stream
   c->grid = std::max(1, std::min({n, blocks, kMaxShares / (2 * dash::kTurns)}));
   // A list of under four chunks a block is one share a block, a longer one shares from the counter.  The two in us, in
   // a graph, by chunks a block: 2.6: 12.8 and 13.9; 4.25: 17.5 and 19.4; 8.1: 27.3 and 29.6; 16: 48.5 and 50.2; 32:
-  // 90.0 and 91.6; 129: 343.6 and 341 (all fp32), and in fp16, where the SMs drift apart most, 395 and 364.  So one
+  // 90.0 and 91.6; 129: 343.6 and 341 (all fp32; in fp16 395 and 364).  So one
   // share is ahead up to some 30 chunks a block already, by 2 to 10%.
   c->rounds = n < 4 * c->grid ? (n + c->grid - 1) / c->grid : std::max(1, n / (dash::kTurns * c->grid));
   // whole groups of grid x rounds chunks, the last one short
