@@ -175,6 +175,23 @@ def _workspace(nbytes, device):
     return torch.empty(max(int(nbytes), 256), dtype=torch.uint8, device=device)
 
 
+def _outputs(stream, device, given, make):
+    """`given`, and in the places of None what `make` allocates there: on
+    `stream`, where it is written.  (What was freed on the current stream may
+    be in its queued work's use still.)  The current stream, which uses them
+    next, holds them too."""
+    if all(t is not None for t in given):
+        return given
+    import torch
+    with torch.cuda.stream(stream):
+        out = [f() if t is None else t for t, f in zip(given, make)]
+    if stream is not None:
+        for t, g in zip(out, given):
+            if g is None:
+                t.record_stream(torch.cuda.current_stream(device))
+    return out
+
+
 def inv_root_workspace_bytes(n, B, solver=SOLVER_NEWTON_DB):
     return int(load().shampoo_inv_root_workspace_bytes(n, B, solver))
 
@@ -185,10 +202,10 @@ def inv_root_newton_db(A, v0, iters1=14, iters2=14, eps=0.0, pi_iters=10, X=None
     Newton-DB path.  Returns (X, lambda, ws)."""
     import torch
     n, B = A.shape[0], A.shape[1]
-    X = torch.empty_like(A) if X is None else X
-    lam = torch.empty(n, dtype=torch.float32, device=A.device) if lam is None else lam
     need = inv_root_workspace_bytes(n, B, SOLVER_NEWTON_DB)
-    ws = _workspace(need, A.device) if ws is None else ws
+    X, lam, ws = _outputs(stream, A.device, (X, lam, ws), (
+        lambda: torch.empty_like(A), lambda: torch.empty(n, dtype=torch.float32, device=A.device),
+        lambda: _workspace(need, A.device)))
     rc = load().shampoo_inv_root_newton_db(_ptr(A), _ptr(X), n, B, iters1, iters2, eps, _ptr(v0), pi_iters,
                                            _ptr(lam), _ptr(ws), ws.numel(), _stream(stream))
     _check(rc, "shampoo_inv_root_newton_db")
@@ -200,10 +217,10 @@ def inv_root_chebyshev(A, v0, degree=16, delta=1e-3, eps=0.0, pi_iters=10, X=Non
     """Chebyshev/Clenshaw variant of :func:`inv_root_newton_db`."""
     import torch
     n, B = A.shape[0], A.shape[1]
-    X = torch.empty_like(A) if X is None else X
-    lam = torch.empty(n, dtype=torch.float32, device=A.device) if lam is None else lam
     need = inv_root_workspace_bytes(n, B, SOLVER_CHEBYSHEV)
-    ws = _workspace(need, A.device) if ws is None else ws
+    X, lam, ws = _outputs(stream, A.device, (X, lam, ws), (
+        lambda: torch.empty_like(A), lambda: torch.empty(n, dtype=torch.float32, device=A.device),
+        lambda: _workspace(need, A.device)))
     rc = load().shampoo_inv_root_chebyshev(_ptr(A), _ptr(X), n, B, degree, delta, eps, _ptr(v0), pi_iters,
                                            _ptr(lam), _ptr(ws), ws.numel(), _stream(stream))
     _check(rc, "shampoo_inv_root_chebyshev")
@@ -219,10 +236,10 @@ def inv_root_coupled_newton(A, v0, iters=16, fp16=False, eps=0.0, pi_iters=10, X
     fp16 products)."""
     import torch
     n, B = A.shape[0], A.shape[1]
-    X = torch.empty_like(A) if X is None else X
-    lam = torch.empty(n, dtype=torch.float32, device=A.device) if lam is None else lam
     need = inv_root_workspace_bytes(n, B, SOLVER_COUPLED_NEWTON)
-    ws = _workspace(need, A.device) if ws is None else ws
+    X, lam, ws = _outputs(stream, A.device, (X, lam, ws), (
+        lambda: torch.empty_like(A), lambda: torch.empty(n, dtype=torch.float32, device=A.device),
+        lambda: _workspace(need, A.device)))
     rc = load().shampoo_inv_root_coupled_newton(_ptr(A), _ptr(X), n, B, iters, 1 if fp16 else 0, eps, _ptr(v0),
                                                 pi_iters, _ptr(lam), _ptr(ws), ws.numel(), _stream(stream))
     _check(rc, "shampoo_inv_root_coupled_newton")
@@ -235,8 +252,8 @@ def inv_root_newton_db_static(A, v0, iters1=14, iters2=14, eps=0.0, pi_iters=10,
     the library; X and lambda are allocated here only if not given)."""
     import torch
     n, B = A.shape[0], A.shape[1]
-    X = torch.empty_like(A) if X is None else X
-    lam = torch.empty(n, dtype=torch.float32, device=A.device) if lam is None else lam
+    X, lam = _outputs(stream, A.device, (X, lam), (
+        lambda: torch.empty_like(A), lambda: torch.empty(n, dtype=torch.float32, device=A.device)))
     rc = load().shampoo_inv_root_newton_db_static(_ptr(A), _ptr(X), n, B, iters1, iters2, eps, _ptr(v0), pi_iters,
                                                   _ptr(lam), _stream(stream))
     _check(rc, "shampoo_inv_root_newton_db_static")
@@ -636,19 +653,10 @@ class AdamW(_TensorList):
         on `stream`: other streams wait for it before they use them."""
         if m is None or v is None:
             import torch
-            made, given = [], m if v is None else v
+            given = m if v is None else v
             of = dtype or (torch.float32 if given is None else given.dtype)
-            # not from the current stream's memory: what was freed there may be in its queued work's use still
-            with torch.cuda.stream(stream):
-                if m is None:
-                    m = torch.empty(self.moment_elems, dtype=of, device=self.device)
-                    made.append(m)
-                if v is None:
-                    v = torch.empty(self.moment_elems, dtype=of, device=self.device)
-                    made.append(v)
-            if stream is not None:  # the caller's stream uses them next
-                for t in made:
-                    t.record_stream(torch.cuda.current_stream(self.device))
+            m, v = _outputs(stream, self.device, (m, v),
+                            (lambda: torch.empty(self.moment_elems, dtype=of, device=self.device),) * 2)
         m_at, v_at = self._flat(m, "m"), self._flat(v, "v")
         if v.dtype != m.dtype or (dtype is not None and m.dtype != dtype):
             raise ValueError("m and v must be of the one type asked for")

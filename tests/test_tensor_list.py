@@ -398,3 +398,43 @@ def test_the_longest_tensors(lib):
         for rows in ([tensor(n=(1 << 38) + 1, **at, **extra)],
                      [tensor(n=1 << 38, **at, **extra), tensor(n=1 << 38, **more)]):
             assert adamw_init(lib, rows)[0] == bd.SHAMPOO_EINVAL  # too long, or the list is
+
+
+@pytest.mark.parametrize("root", ["newton_db", "chebyshev", "coupled_newton", "newton_db_static"])
+def test_roots_come_from_the_memory_of_the_stream_that_writes_them(monkeypatch, root):
+    torch = pytest.importorskip("torch")
+    import contextlib
+    import types
+    ours, side = (types.SimpleNamespace(cuda_stream=h) for h in (7, 8))
+    current = [ours]
+
+    @contextlib.contextmanager
+    def stream(s):
+        current.append(current[-1] if s is None else s)
+        yield
+        current.pop()
+
+    calls = []
+
+    def call(*args):
+        calls.append(args)
+        return 0
+
+    fake = types.SimpleNamespace(stream=stream, current_stream=lambda device=None: current[-1])
+    fresh = lambda *a, **kw: FakeMemory(1024, None, current[-1])
+    lib = types.SimpleNamespace(shampoo_inv_root_workspace_bytes=lambda *a: 1024, **{f"shampoo_inv_root_{root}": call})
+    monkeypatch.setattr(bd, "_lib", lib)
+    monkeypatch.setattr(torch, "cuda", fake)
+    for name in ("empty", "empty_like"):
+        monkeypatch.setattr(torch, name, fresh)
+    A = FakeMemory(1024, torch.float32, ours)
+    A.shape, A.device = (1, 32, 32), None
+    for s in (None, side):
+        for given in ({}, {"X": FakeMemory(1024, None, ours)}):
+            out = getattr(bd, f"inv_root_{root}")(A, FakeMemory(1, None, ours), stream=s, **given)
+            assert calls[-1][-1].value == (7 if s is None else 8) and current == [ours]
+            for t in out:
+                if t is given.get("X"):
+                    assert not t.recorded
+                else:
+                    assert t.on is (ours if s is None else side) and t.recorded == ([] if s is None else [ours])
