@@ -330,10 +330,10 @@ SHAMPOO_API void shampoo_destroy(shampoo_ctx* ctx);
  * All other calls take the same workspace (SHAMPOO_EINVAL for another one, and
  * for a device scalar that is not aligned to its 4 bytes), are stream-ordered
  * and can be captured into a CUDA graph; bind cannot (SHAMPOO_EINVAL on a
- * capturing stream).  Neither the workspace nor a buffer that a call writes
- * shares memory with another buffer of the call or list, nor do the moments
- * that load reads with what it writes (SHAMPOO_EINVAL).  Calls on one
- * workspace must not overlap.  The
+ * capturing stream).  The workspace shares no memory with the list or with a
+ * buffer that a call is given, and no such buffer does with what the call
+ * reads or writes of the list, nor a written one with another
+ * (SHAMPOO_EINVAL).  Calls on one workspace must not overlap.  The
  * workspace's first word is the status word of its last norm, clip, step or
  * load call (shampoo_read_status).
  * ---------------------------------------------------------------------- */

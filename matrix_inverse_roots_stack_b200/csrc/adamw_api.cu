@@ -23,7 +23,7 @@ struct shampoo_adamw {
   int64_t blocks = 0, tiles = 0;
   size_t off_tensors = 0, total = 0;  // workspace
   const void* bound_ws = nullptr;
-  dash::ListMemory all, written;  // the list's arrays, and those that calls write
+  dash::ListMemory all, written, moments;  // the list's arrays, those that steps write, and the moments with their scales
   dash::AdamwLaunch launch{};
 };
 
@@ -69,6 +69,20 @@ bool wide_ok(const shampoo_adamw_tensor& q) {
                             : dash::aligned_to(q.m_scale, 4) && dash::aligned_to(q.v_scale, 4);
 }
 
+size_t blocks_of(const shampoo_adamw_tensor& q) {
+  return (static_cast<size_t>(q.n) + dash::kQBlock - 1) / dash::kQBlock;
+}
+
+void add_moments(std::vector<dash::ByteRange>& r, const shampoo_adamw_tensor& q) {
+  const size_t bytes = static_cast<size_t>(q.n) * (q.state_bits == 32 ? 4 : 1);
+  dash::add_range(r, q.m, bytes, true);
+  dash::add_range(r, q.v, bytes, true);
+  if (q.state_bits == 8) {
+    dash::add_range(r, q.m_scale, blocks_of(q), true);
+    dash::add_range(r, q.v_scale, blocks_of(q), true);
+  }
+}
+
 void add_tensor(shampoo_adamw* c, const shampoo_adamw_tensor& q, int index) {
   const bool eight = q.state_bits == 8;
   AdamwTensorDev r{};
@@ -92,7 +106,7 @@ void add_tensor(shampoo_adamw* c, const shampoo_adamw_tensor& q, int index) {
   c->bits = c->tensors.empty() || c->bits == q.state_bits ? q.state_bits : 0;
   c->first_tile.push_back(r.first_tile);
   c->tensors.push_back(r);
-  c->blocks += (q.n + dash::kQBlock - 1) / dash::kQBlock;
+  c->blocks += static_cast<int64_t>(blocks_of(q));
   c->tiles += (q.n + dash::kTile - 1) / dash::kTile;
   c->stage_bytes = std::max(c->stage_bytes, dash::adamw_stage_bytes(eight, q.param_dtype, q.grad_dtype));
 }
@@ -159,18 +173,12 @@ int shampoo_adamw_init(shampoo_adamw** out, const shampoo_adamw_tensor* tensors,
       const shampoo_adamw_tensor& q = tensors[i];
       ok = tensor_ok(q);
       if (!ok || q.n == 0) continue;
-      const size_t n = static_cast<size_t>(q.n), ms = q.state_bits == 32 ? 4 : 1;
-      const size_t blocks = (n + dash::kQBlock - 1) / dash::kQBlock;
-      blocks_total += static_cast<int64_t>(blocks);
+      const size_t n = static_cast<size_t>(q.n);
+      blocks_total += static_cast<int64_t>(blocks_of(q));
       dash::add_range(ranges, q.param, n * dash::dtype_bytes(q.param_dtype), true);
       dash::add_range(ranges, q.grad, n * dash::dtype_bytes(q.grad_dtype), false);
       if (q.copy) dash::add_range(ranges, q.copy, 2 * n, true);
-      dash::add_range(ranges, q.m, n * ms, true);
-      dash::add_range(ranges, q.v, n * ms, true);
-      if (q.state_bits == 8) {
-        dash::add_range(ranges, q.m_scale, blocks, true);
-        dash::add_range(ranges, q.v_scale, blocks, true);
-      }
+      add_moments(ranges, q);
     }
     if (!ok || blocks_total > kMaxBlocks || dash::ranges_clash(ranges)) {
       delete c;
@@ -178,6 +186,10 @@ int shampoo_adamw_init(shampoo_adamw** out, const shampoo_adamw_tensor* tensors,
     }
     c->all = dash::ListMemory(ranges, false);
     c->written = dash::ListMemory(ranges, true);
+    std::vector<dash::ByteRange> moments;
+    for (int i = 0; i < n_tensors; ++i) add_moments(moments, tensors[i]);
+    std::sort(moments.begin(), moments.end(), [](const auto& a, const auto& b) { return a.lo < b.lo; });
+    c->moments = dash::ListMemory(moments, true);
     for (int i = 0; i < n_tensors; ++i)
       if (tensors[i].n > 0) add_tensor(c, tensors[i], i);
     if (c->tensors.empty()) c->stage_bytes = dash::adamw_stage_bytes(false, SHAMPOO_DTYPE_F32, SHAMPOO_DTYPE_F32);
@@ -267,8 +279,8 @@ int shampoo_adamw_load_moments(shampoo_adamw* c, const float* m, const float* v,
   const int rc = check_bound(c, ws, ws_bytes);
   if (rc) return rc;
   const size_t bytes = flat_bytes(c, SHAMPOO_DTYPE_F32);
-  if (!flat_ok(c, m) || !flat_ok(c, v) || !apart(c, c->written, m, bytes, ws) ||
-      !apart(c, c->written, v, bytes, ws))
+  if (!flat_ok(c, m) || !flat_ok(c, v) || !apart(c, c->moments, m, bytes, ws) ||
+      !apart(c, c->moments, v, bytes, ws))
     return SHAMPOO_EINVAL;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (cudaMemsetAsync(ws, 0, sizeof(unsigned), st) != cudaSuccess) return SHAMPOO_ECUDA;
@@ -284,7 +296,7 @@ int shampoo_adamw_read_moments(shampoo_adamw* c, void* m, void* v, int dtype, vo
   if ((dtype != SHAMPOO_DTYPE_F32 && dtype != SHAMPOO_DTYPE_BF16) || !flat_ok(c, m) || !flat_ok(c, v))
     return SHAMPOO_EINVAL;
   const size_t bytes = flat_bytes(c, dtype);
-  if (dash::share(m, bytes, v, bytes) || !apart(c, c->all, m, bytes, ws) || !apart(c, c->all, v, bytes, ws))
+  if (dash::share(m, bytes, v, bytes) || !apart(c, c->moments, m, bytes, ws) || !apart(c, c->moments, v, bytes, ws))
     return SHAMPOO_EINVAL;
   if (c->blocks == 0) return SHAMPOO_OK;
   dash::launch_read_moments(table(c, ws), m, v, dtype, static_cast<cudaStream_t>(stream));

@@ -230,7 +230,8 @@ int norm_pass(shampoo_grads* c, float max_norm, float inv_scale, float* out, voi
     return SHAMPOO_EINVAL;
   if (!ws || ws_bytes < c->total) return SHAMPOO_EWORKSPACE;
   if (ws != c->bound_ws) return SHAMPOO_EINVAL;
-  if (c->memory.meets(out, 2 * sizeof(float)) || dash::share(out, 2 * sizeof(float), ws, c->total)) return SHAMPOO_EINVAL;
+  if ((clip && c->memory.meets(out, 2 * sizeof(float))) || dash::share(out, 2 * sizeof(float), ws, c->total))
+    return SHAMPOO_EINVAL;
   char* w = static_cast<char*>(ws);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const auto* table = reinterpret_cast<const dash::GradChunk*>(w + dash::kHeaderBytes);

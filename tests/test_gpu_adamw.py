@@ -811,15 +811,26 @@ def test_buffers_that_share_memory_are_refused(torch, bd):
         opt.load_moments(*ok)
         opt.load_moments(ok[0], ok[0])  # both are only read
         opt.load_moments(g, ok[0])
-        for m, v in [(ok[0], ok[0]), (big[4:n + 4], ok[0]), (ok[1], big[n + 8:]), (p, ok[0]), (ok[0], p), (g, ok[0]),
-                     (ok[1], g)] + [(t, ok[0]) for t in own] + [(ok[0], t) for t in own]:
+        for m, v in [(ok[0], ok[0]), (big[4:n + 4], ok[0]), (ok[1], big[n + 8:])] + \
+                [(t, ok[0]) for t in own] + [(ok[0], t) for t in own]:
             with pytest.raises(bd.ShampooError):
                 opt.read_moments(m=m, v=v)
+        opt.read_moments(m=g, v=ok[0])  # the call has nothing else to do with gradients and parameters
+        opt.load_moments(p, g)
+        if bits == 8:  # codes, or scales, cut from a flat tensor
+            for cut in ("m", "v", "m_scale", "v_scale"):
+                flat, other = z(), z()
+                k = n if len(cut) == 1 else 2
+                inside = bd.AdamW([p], [g], state_bits=8, **{cut: [flat.view(torch.uint8)[100:100 + k]]})
+                for f in (lambda: inside.read_moments(m=flat, v=other), lambda: inside.read_moments(m=other, v=flat),
+                          lambda: inside.load_moments(flat, other), lambda: inside.load_moments(other, flat)):
+                    with pytest.raises(bd.ShampooError):
+                        f()
         half = big.view(torch.bfloat16)
         opt.read_moments(m=half[:n], v=half[n:2 * n])
         with pytest.raises(bd.ShampooError):
             opt.read_moments(m=half[:n], v=half[n - 8:2 * n - 8])
-        for m, v in [(p, ok[0]), (ok[0], p)] + [(t, ok[0]) for t in own] + [(ok[0], t) for t in own]:
+        for m, v in [(t, ok[0]) for t in own] + [(ok[0], t) for t in own]:
             with pytest.raises(bd.ShampooError):
                 opt.load_moments(m, v)
         for s in [p[7:8]] + [t[:1] for t in own]:
@@ -828,9 +839,11 @@ def test_buffers_that_share_memory_are_refused(torch, bd):
                     opt.step(**kw)
         opt.step(g[3:4], coef=big[:1])  # a gradient is only read: lr 0
         lib, stream = bd.load(), torch.cuda.current_stream().cuda_stream
-        for fn in (lib.shampoo_grad_norm, lib.shampoo_grad_clip):
-            for at in (g.data_ptr(), g.data_ptr() + 4 * n - 4, g.data_ptr() - 4, clip.ws.data_ptr() + 8):
-                assert fn(clip._ctx, 1.0, 1.0, at, clip.ws.data_ptr(), clip.ws.numel(), stream) == bd.SHAMPOO_EINVAL
+        for at in (g.data_ptr(), g.data_ptr() + 4 * n - 4, g.data_ptr() - 4, clip.ws.data_ptr() + 8):
+            assert lib.shampoo_grad_clip(clip._ctx, 1.0, 1.0, at, clip.ws.data_ptr(), clip.ws.numel(),
+                                         stream) == bd.SHAMPOO_EINVAL
+        assert lib.shampoo_grad_norm(clip._ctx, 1.0, 1.0, clip.ws.data_ptr() + 8, clip.ws.data_ptr(), clip.ws.numel(),
+                                     stream) == bd.SHAMPOO_EINVAL
         assert opt.status() == (0, 0) and clip.norm().tolist() == [0.0, 1.0] and not bool(p.any())
 
 
